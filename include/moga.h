@@ -356,6 +356,111 @@ moga_status moga_layer_ex(const void* x, const void* W_r, const float* b_r, moga
                           int Wg, const int* window, int branches, void* out, int32_t* group_id, float* gate,
                           int32_t* perm, int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- queries and keys before the block
+ * moga_qk_norm_rope: the norm of every query and key head and the rotation by
+ * the token's place, in one pass: it makes the q and k that the attention
+ * calls take.  For a head x of d_h channels and its weight w:
+ *   r = 1 / sqrt(mean_c x_c^2 + eps),  z_c = w_c x_c r,
+ *   y_a = z_a cos t - z_b sin t,  y_b = z_a sin t + z_b cos t
+ * for each pair (a, b) of channels, t = position on the pair's axis times the
+ * pair's frequency.  Pair j is channels (2j, 2j+1) (halves = 0) or
+ * (j, j + d_h/2) (halves = 1).  The first axes[0] pairs turn with axis 0
+ * (frame), the next axes[1] with axis 1 (row), the next axes[2] with axis 2
+ * (column); pairs past them do not turn.
+ * In:  q [N, H_q, d_h], k [N, H_k, d_h] of type dt, a token and a head stride
+ *      each in elements (multiples of 16 bytes; d_h channels dense), so that
+ *      both may lie in one packed projection; H_q = 0 or H_k = 0 leaves that
+ *      side out.  w_q, w_k fp32 [d_h] or NULL (ones).
+ *      table fp32 [P, d_h/2, 2]: (cos, sin) of pair j at position p, as
+ *      moga_rope_table makes it; NULL: the norm alone (then pos and grid are
+ *      NULL too).  With a table, exactly one of
+ *        grid (HOST int[3]) = (T, Hg, Wg): token n lies at place
+ *             (token0 + n) mod (T*Hg*Wg) in frame, row, column order;
+ *             0 <= token0 < T*Hg*Wg, and no turning axis is longer than P;
+ *        pos (device int32 [N, 3]): the three positions of each token, in
+ *             [0, P) on the axes that turn.  Checked on the device: a token
+ *             outside is skipped and moga_sync_status() reports
+ *             MOGA_ERR_DEVICE_CHECK.
+ *      axes is HOST int[3].
+ * Out: q_out, k_out bf16 [N, H, d_h], dense.  A bf16, dense input may be its
+ *      own output; any other overlap is not allowed.
+ * The sums and the rotation are fp32; an output is rounded once.
+ * Limits: d_h 64 or 128, H up to 65536, eps >= 0 and finite.
+ * Workspace: moga_qk_norm_rope_workspace_size() bytes, needed with pos only
+ * (ws may be NULL otherwise). */
+size_t moga_qk_norm_rope_workspace_size(void);
+moga_status moga_qk_norm_rope(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k,
+                              int64_t k_stride_n, int64_t k_stride_h, moga_dtype dt, int64_t N, int H_q, int H_k,
+                              int d_h, const float* w_q, const float* w_k, float eps, const float* table, int P,
+                              const int* axes, const int* grid, int64_t token0, const int32_t* pos, int halves,
+                              void* q_out, void* k_out, void* ws, size_t ws_bytes, void* stream);
+
+/* moga_rope_table: table fp32 [P, d_h/2, 2] of (cos, sin) of p * theta^(-i/n)
+ * for the i-th of an axis's n pairs ((1, 0) for pairs that do not turn); the
+ * angles are formed in 64 bits.  axes: HOST int[3], their sum at most d_h/2. */
+moga_status moga_rope_table(int P, int d_h, const int* axes, double theta, float* table, void* stream);
+
+/* moga_qk_norm_rope_backward: gradients of moga_qk_norm_rope from dq_out,
+ * dk_out (bf16 [N, H, d_h], dense) and the forward's arguments.
+ * Out: dq, dk of type dt [N, H, d_h], dense; dw_q, dw_k fp32 [d_h] (each may
+ * be NULL), overwritten, summed in a fixed order.  A token whose listed
+ * position is outside the table is skipped (its dq, dk are not written).
+ * Workspace: moga_qk_norm_rope_backward_workspace_size(d_h) bytes. */
+size_t moga_qk_norm_rope_backward_workspace_size(int d_h);
+moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, int64_t q_stride_n,
+                                       int64_t q_stride_h, const void* k, int64_t k_stride_n, int64_t k_stride_h,
+                                       moga_dtype dt, int64_t N, int H_q, int H_k, int d_h, const float* w_q,
+                                       const float* w_k, float eps, const float* table, int P, const int* axes,
+                                       const int* grid, int64_t token0, const int32_t* pos, int halves, void* dq,
+                                       void* dk, float* dw_q, float* dw_k, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- cross attention
+ * moga_cross_attn: attention of N query tokens to L rows of an encoder's
+ * states (the text blocks between the visual blocks: each shot's tokens
+ * attend to that shot's own prompt, "Cross-modal attention").  Segment s has
+ * queries [q_offsets[s], q_offsets[s+1]) and keys [kv_offsets[s],
+ * kv_offsets[s] + kv_lens[s]):
+ *   out = softmax(Q K^T / sqrt(d_h)) V   per segment and head;
+ * query head h reads key head h / (H / H_kv).
+ * In:  q bf16 [N, H, d_h], k, v bf16 [L, H_kv, d_h], a token and a head
+ *      stride each in elements (multiples of 8): token-major (a token's heads
+ *      inside its stride) or head-major (the head stride a whole number, N or
+ *      L at least, of token strides).
+ *      q_offsets, kv_offsets device int32 [S+1], rising from 0 or more to at
+ *      most N and L; NULL (only with S = 1): all rows.  kv_lens device int32
+ *      [S], at most the distance to the next offset; NULL: all of it.
+ *      Checked on the device: a violation skips all work and
+ *      moga_sync_status() reports MOGA_ERR_DEVICE_CHECK.
+ * Out: out bf16 [N, H, d_h], dense; lse fp32 [H, N] or NULL: the natural
+ *      log-sum-exp of each query's scaled scores.  A query whose segment has
+ *      no keys gets out = 0 and lse = -inf.  Rows of no segment are left as
+ *      they were.  Values of rows that no segment reads (padding) have no
+ *      effect, infinities and NaN included.
+ * Limits: d_h 64 or 128; N, L < 2^30; N * H, L * H_kv < 2^31; H a multiple
+ * of H_kv; S <= 1024.
+ * Workspace: moga_cross_attn_workspace_size(...) bytes. */
+size_t moga_cross_attn_workspace_size(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
+moga_status moga_cross_attn(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k, int64_t k_stride_n,
+                            int64_t k_stride_h, const void* v, int64_t v_stride_n, int64_t v_stride_h, int64_t N,
+                            int64_t L, int H, int H_kv, int d_h, const int32_t* q_offsets, const int32_t* kv_offsets,
+                            const int32_t* kv_lens, int S, void* out, float* lse, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* moga_cross_attn_backward: gradients of moga_cross_attn from dout (bf16
+ * [N, H, d_h], dense), the forward's inputs and its out and lse.
+ * Out: dq bf16 [N, H, d_h], dk, dv bf16 [L, H_kv, d_h], dense; dk and dv are
+ *      summed over the query heads that share a key head.  Rows of no segment
+ *      (and key rows past a segment's length) are left as they were.  All sums
+ *      are taken in a fixed order.
+ * Workspace: moga_cross_attn_backward_workspace_size(...) bytes. */
+size_t moga_cross_attn_backward_workspace_size(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
+moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_stride_n, int64_t q_stride_h,
+                                     const void* k, int64_t k_stride_n, int64_t k_stride_h, const void* v,
+                                     int64_t v_stride_n, int64_t v_stride_h, int64_t N, int64_t L, int H, int H_kv,
+                                     int d_h, const int32_t* q_offsets, const int32_t* kv_offsets,
+                                     const int32_t* kv_lens, int S, const void* out, const float* lse, void* dq,
+                                     void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- host pipeline
  * A pipeline runs the visual block of moga_layer_ex (same arithmetic, same
  * branches) on inputs that live in HOST memory and returns the output to host

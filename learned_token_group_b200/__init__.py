@@ -21,7 +21,9 @@ import torch
 __all__ = ["MogaError", "get_lib", "LIB_PATH", "HEADER_PATH", "route", "group_attn", "stga_window_attn",
            "moga_layer", "sync_status", "workspace", "MogaLayer", "exported_names", "kernel_launches",
            "set_timing_events", "STAGES", "Pipeline", "stga_shot_attn", "moga_layer_shots", "sort",
-           "layer_train", "layer_backward", "MogaFunction"]
+           "layer_train", "layer_backward", "MogaFunction", "rope_table", "qk_norm_rope", "qk_norm_rope_backward",
+           "QkNormRopeFunction", "cross_attn_workspace_size", "cross_attn", "cross_attn_backward",
+           "CrossAttnFunction"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoga.so")
@@ -40,6 +42,7 @@ class MogaError(RuntimeError):
 
 _lib = None
 _P, _I64, _I, _F, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_D = ctypes.c_double
 
 
 def get_lib():
@@ -96,6 +99,19 @@ def get_lib():
                                         _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
         "moga_layer_backward": (_I, [_P, _P, _P, _P, _I, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _P,
                                      _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+        "moga_rope_table": (_I, [_I, _I, _P, _D, _P, _P]),
+        "moga_qk_norm_rope_workspace_size": (_SZ, []),
+        "moga_qk_norm_rope": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P,
+                                   _I64, _P, _I, _P, _P, _P, _SZ, _P]),
+        "moga_qk_norm_rope_backward_workspace_size": (_SZ, [_I]),
+        "moga_qk_norm_rope_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F,
+                                            _P, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+        "moga_cross_attn_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
+        "moga_cross_attn": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P,
+                                 _I, _P, _P, _P, _SZ, _P]),
+        "moga_cross_attn_backward_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
+        "moga_cross_attn_backward": (_I, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I,
+                                          _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -503,6 +519,307 @@ class MogaFunction(torch.autograd.Function):
                            window, balance_alpha=alpha)
         db = g["db_r"] if ctx.b_r is not None else None
         return g["dx"], g["dW_r"].to(W_r.dtype), db, g["dq"], g["dk"], g["dv"], None, None, None, None, None
+
+
+# ----------------------------------------------------------------------------- queries and keys, cross attention
+def _on(dev: torch.device, **tensors):
+    """Every given tensor must be on the CUDA device ``dev``."""
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} must be on {dev}, got {t.device}")
+
+
+def _rows(t: torch.Tensor, name: str, dtypes):
+    """A [tokens, heads, d_h] tensor or view whose heads are dense: its shape and its two strides."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d_h], got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.stride(2) != 1:
+        raise ValueError(f"{name}'s heads must be dense")
+    return t.shape, t.stride()
+
+
+def _readable(t: Optional[torch.Tensor], head_major: bool = False):
+    """t itself where the kernels read it in place, else a dense copy (autograd's inputs may be any view)."""
+    if t is None or t.dim() != 3 or not t.is_cuda:
+        return t
+    unit = 16 // t.element_size()
+    n, h, d = t.shape
+    sn, sh = t.stride(0) if n > 1 else h * d, t.stride(1) if h > 1 else d
+    ok = t.stride(2) == 1 and t.data_ptr() % 16 == 0 and sn % unit == 0 and sh % unit == 0 and sh >= d
+    ok = ok and (sn >= (h - 1) * sh + d or (head_major and sn >= d and sh % sn == 0 and sh // sn >= n))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
+    _on(dev, **{name: t})
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t
+
+
+def _call(dev: torch.device, what: str, *args):
+    """Calls the library on ``dev`` and its current stream (the last argument)."""
+    fn = getattr(get_lib(), what)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        raise MogaError(st, what)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def rope_table(P: int, d_h: int, axes: Sequence[int], theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """(cos, sin) of every pair at positions 0 .. P - 1, fp32 [P, d_h / 2, 2] (moga_rope_table in moga.h).
+
+    axes: how many pairs turn with the token's frame, row and column."""
+    dev = torch.device(device)
+    dev = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+    if P < 1 or d_h not in (64, 128):
+        raise ValueError(f"a table needs P >= 1 positions and d_h 64 or 128, got {P} and {d_h}")
+    table = torch.empty((P, d_h // 2, 2), dtype=torch.float32, device=dev)
+    _call(dev, "moga_rope_table", P, d_h, _int3(axes), float(theta), _at(table))
+    return table
+
+
+def _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves):
+    """Checks the shared arguments: (device, N, heads, d_h, the C call's arguments from q on)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("one of q and k must be given")
+    (N, _, d_h), _ = _rows(x, "q" if q is not None else "k", (torch.bfloat16, torch.float32))
+    dev, args, heads = x.device, [], []
+    for n, t in (("q", q), ("k", k)):
+        if t is None:
+            args += [None, 0, 0]
+            heads.append(0)
+            continue
+        shape, st = _rows(t, n, (x.dtype,))
+        if shape[0] != N or shape[2] != d_h:
+            raise ValueError(f"q and k must have the same tokens and d_h, got {tuple(x.shape)} and {tuple(shape)}")
+        _on(dev, **{n: t})
+        args += [t.data_ptr(), st[0], st[1]]
+        heads.append(shape[1])
+    for n, w in (("w_q", w_q), ("w_k", w_k)):
+        if w is not None:
+            _dense(w, n, (d_h,), torch.float32, dev)
+    P, axes3, grid3 = 0, None, None
+    if table is not None:
+        if table.dim() != 3 or axes is None:
+            raise ValueError("a table is [P, d_h / 2, 2] and needs axes")
+        P, axes3 = table.shape[0], _int3(axes)
+        _dense(table, "table", (P, d_h // 2, 2), torch.float32, dev)
+        if (grid is None) == (positions is None):
+            raise ValueError("a table needs a grid or positions, one of them")
+        grid3 = None if grid is None else _int3(grid)
+    elif grid is not None or positions is not None:
+        raise ValueError("grid and positions need a table")
+    if positions is not None:
+        _dense(positions, "positions", (N, 3), torch.int32, dev)
+    dt = MOGA_BF16 if x.dtype == torch.bfloat16 else MOGA_F32
+    args += [dt, N, heads[0], heads[1], d_h, _at(w_q), _at(w_k), float(eps), _at(table), P, axes3, grid3,
+             int(token0), _at(positions), int(bool(halves))]
+    return dev, N, heads, d_h, args
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], w_q: Optional[torch.Tensor] = None,
+                 w_k: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+                 axes: Optional[Sequence[int]] = None, grid: Optional[Sequence[int]] = None,
+                 positions: Optional[torch.Tensor] = None, token0: int = 0, eps: float = 1e-6, halves: bool = False,
+                 out=None, ws: Optional[torch.Tensor] = None):
+    """Norm of every query and key head and rotation by the token's place (moga_qk_norm_rope in moga.h).
+
+    q [N, H, d_h], k [N, H_k, d_h] (bf16 or fp32; views of a packed projection
+    are read in place; either may be None).  table (``rope_table``) with its
+    axes and a grid (T, Hg, Wg), token0 being the first token's place on it, or
+    with positions int32 [N, 3]; without a table the norm alone.  Returns
+    (q_out, k_out), bf16 and dense, None for a side that was None; out: such a
+    pair to write to.  ws (``workspace``): for positions outside the table,
+    which ``sync_status`` reports; it is made when positions are given without it."""
+    dev, N, heads, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+    outs = [None, None]
+    for i, n in enumerate(("q_out", "k_out")):
+        if heads[i]:
+            shape = (N, heads[i], d_h)
+            outs[i] = (torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None
+                       else _dense(out[i], n, shape, torch.bfloat16, dev))
+    if ws is None and positions is not None:
+        ws = workspace(256, dev)
+    _on(dev, ws=ws)
+    _call(dev, "moga_qk_norm_rope", *args, _at(outs[0]), _at(outs[1]), _at(ws), 0 if ws is None else ws.numel())
+    return outs[0], outs[1]
+
+
+def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                          k: Optional[torch.Tensor], w_q: Optional[torch.Tensor] = None,
+                          w_k: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+                          axes: Optional[Sequence[int]] = None, grid: Optional[Sequence[int]] = None,
+                          positions: Optional[torch.Tensor] = None, token0: int = 0, eps: float = 1e-6,
+                          halves: bool = False, ws: Optional[torch.Tensor] = None):
+    """Gradients of ``qk_norm_rope`` (moga_qk_norm_rope_backward in moga.h):
+    dict(dq, dk, dw_q, dw_k, ws) from the gradients of its outputs (bf16,
+    dense).  dq and dk have the inputs' type; dw_q, dw_k are fp32 [d_h], None
+    for a weight that is None.  Pass the ws back to reuse it."""
+    dev, N, heads, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+    g = {"dq": None, "dk": None, "dw_q": None, "dw_k": None}
+    for i, (n, d, x, w) in enumerate((("q", dq_out, q, w_q), ("k", dk_out, k, w_k))):
+        if not heads[i]:
+            continue
+        if d is None:
+            raise ValueError(f"d{n}_out is missing")
+        _dense(d, f"d{n}_out", (N, heads[i], d_h), torch.bfloat16, dev)
+        g[f"d{n}"] = torch.empty((N, heads[i], d_h), dtype=x.dtype, device=dev)
+        if w is not None:
+            g[f"dw_{n}"] = torch.empty(d_h, dtype=torch.float32, device=dev)
+    need = get_lib().moga_qk_norm_rope_backward_workspace_size(d_h)
+    if ws is None or ws.numel() < need:
+        ws = workspace(need, dev)
+    _on(dev, ws=ws)
+    _call(dev, "moga_qk_norm_rope_backward", _at(dq_out) if heads[0] else None, _at(dk_out) if heads[1] else None,
+          *args, _at(g["dq"]), _at(g["dk"]), _at(g["dw_q"]), _at(g["dw_k"]), _at(ws), ws.numel())
+    g["ws"] = ws
+    return g
+
+
+class QkNormRopeFunction(torch.autograd.Function):
+    """``qk_norm_rope`` under torch.autograd: q_out, k_out =
+    QkNormRopeFunction.apply(q, k, w_q, w_k, table, axes, grid, positions,
+    token0, eps, halves).  q, k, w_q, w_k get gradients.  q and k may be views;
+    those the kernels cannot read in place are copied."""
+
+    @staticmethod
+    def forward(ctx, q, k, w_q=None, w_k=None, table=None, axes=None, grid=None, positions=None, token0=0, eps=1e-6,
+                halves=False):
+        q, k = _readable(q), _readable(k)
+        ctx.save_for_backward(q, k, w_q, w_k, table, positions)
+        ctx.args = (axes, grid, token0, eps, halves)
+        return qk_norm_rope(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, w_q, w_k, table, positions = ctx.saved_tensors
+        axes, grid, token0, eps, halves = ctx.args
+        full = lambda d, x: None if x is None else (  # noqa: E731
+            torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device) if d is None
+            else d.to(torch.bfloat16).contiguous())
+        g = qk_norm_rope_backward(full(dq_out, q), full(dk_out, k), q, k, w_q, w_k, table, axes, grid, positions,
+                                  token0, eps, halves)
+        return g["dq"], g["dk"], g["dw_q"], g["dw_k"], None, None, None, None, None, None, None
+
+
+def _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens):
+    """Checks the shared arguments: (device, N, L, H, H_kv, d_h, S, the C call's arguments from q on)."""
+    (N, H, d_h), qs = _rows(q, "q", (torch.bfloat16,))
+    (L, Hk, dk), ks = _rows(k, "k", (torch.bfloat16,))
+    sv, vs = _rows(v, "v", (torch.bfloat16,))
+    if dk != d_h or tuple(sv) != (L, Hk, dk) or Hk == 0 or H % Hk:
+        raise ValueError(f"k and v must be [L, H_kv, {d_h}] with H_kv dividing {H}, got {tuple(k.shape)} and {tuple(sv)}")
+    dev = q.device
+    _on(dev, k=k, v=v)
+    if (q_offsets is None) != (kv_offsets is None) and (q_offsets if kv_offsets is None else kv_offsets).numel() != 2:
+        raise ValueError("several segments need q_offsets and kv_offsets")
+    S = 1
+    for n, t in (("q_offsets", q_offsets), ("kv_offsets", kv_offsets)):
+        if t is not None:
+            if t.dim() != 1 or t.numel() < 2:
+                raise ValueError(f"{n} must be int32 [S + 1]")
+            S = t.numel() - 1
+    for n, t, m in (("q_offsets", q_offsets, S + 1), ("kv_offsets", kv_offsets, S + 1), ("kv_lens", kv_lens, S)):
+        if t is not None:
+            _dense(t, n, (m,), torch.int32, dev)
+    # the stride of a dimension of one element says nothing
+    st = lambda t, s: (s[0] if t.shape[0] > 1 else t.shape[1] * d_h, s[1] if t.shape[1] > 1 else d_h)  # noqa: E731
+    args = [q.data_ptr(), *st(q, qs), k.data_ptr(), *st(k, ks), v.data_ptr(), *st(v, vs), N, L, H, Hk, d_h,
+            _at(q_offsets), _at(kv_offsets), _at(kv_lens), S]
+    return dev, N, L, H, Hk, d_h, S, args
+
+
+def cross_attn_workspace_size(q: torch.Tensor, k: torch.Tensor, segments: int = 1, backward: bool = False) -> int:
+    """Bytes of a workspace that ``cross_attn`` (and, with backward, ``cross_attn_backward``) takes for these shapes."""
+    lib = get_lib()
+    args = (q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], segments)
+    n = lib.moga_cross_attn_workspace_size(*args)
+    return max(n, lib.moga_cross_attn_backward_workspace_size(*args)) if backward else n
+
+
+def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+               kv_offsets: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
+               return_lse: bool = False, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Cross attention of q [N, H, d_h] to k, v [L, H_kv, d_h] (moga_cross_attn in moga.h); bf16, views read in place.
+
+    Segment s: queries q_offsets[s] to q_offsets[s + 1], keys kv_offsets[s] on,
+    kv_lens[s] of them (by default up to the next offset); device int32.
+    Without offsets all queries attend to all keys.  Returns out [N, H, d_h],
+    or (out, lse [H, N]) with return_lse.  Rows of no segment are zero (lse
+    -inf) in an output made here, and left as they were in a given ``out``."""
+    dev, N, L, H, Hk, d_h, S, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
+    if out is None:
+        make = torch.empty if q_offsets is None else torch.zeros
+        out = make((N, H, d_h), dtype=torch.bfloat16, device=dev)
+    else:
+        _dense(out, "out", (N, H, d_h), torch.bfloat16, dev)
+    lse = None
+    if return_lse:
+        lse = (torch.empty((H, N), dtype=torch.float32, device=dev) if q_offsets is None
+               else torch.full((H, N), float("-inf"), dtype=torch.float32, device=dev))
+    need = get_lib().moga_cross_attn_workspace_size(N, L, H, Hk, d_h, S)
+    if ws is None:
+        ws = workspace(need, dev)
+    _on(dev, ws=ws)
+    _call(dev, "moga_cross_attn", *args, out.data_ptr(), _at(lse), ws.data_ptr(), ws.numel())
+    return (out, lse) if return_lse else out
+
+
+def cross_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                        lse: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+                        kv_offsets: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None):
+    """Gradients of ``cross_attn`` (moga_cross_attn_backward in moga.h): dict(dq,
+    dk, dv, ws), bf16 and dense, from dout and the forward's out and lse.  Rows
+    of no segment get zero.  Pass the ws back to reuse it."""
+    dev, N, L, H, Hk, d_h, S, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
+    _dense(dout, "dout", (N, H, d_h), torch.bfloat16, dev)
+    _dense(out, "out", (N, H, d_h), torch.bfloat16, dev)
+    _dense(lse, "lse", (H, N), torch.float32, dev)
+    make_q = torch.empty if q_offsets is None else torch.zeros
+    make_k = torch.empty if kv_offsets is None and kv_lens is None else torch.zeros
+    dq = make_q((N, H, d_h), dtype=torch.bfloat16, device=dev)
+    dk, dv = (make_k((L, Hk, d_h), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    need = get_lib().moga_cross_attn_backward_workspace_size(N, L, H, Hk, d_h, S)
+    if ws is None or ws.numel() < need:
+        ws = workspace(need, dev)
+    _on(dev, ws=ws)
+    _call(dev, "moga_cross_attn_backward", dout.data_ptr(), *args, out.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+          dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel())
+    return {"dq": dq, "dk": dk, "dv": dv, "ws": ws}
+
+
+class CrossAttnFunction(torch.autograd.Function):
+    """``cross_attn`` under torch.autograd: out = CrossAttnFunction.apply(q, k,
+    v, q_offsets, kv_offsets, kv_lens); q, k and v get gradients.  The inputs
+    may be views; those the kernels cannot read in place are copied."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, q_offsets=None, kv_offsets=None, kv_lens=None):
+        q, k, v = (_readable(t, head_major=True) for t in (q, k, v))
+        out, lse = cross_attn(q, k, v, q_offsets, kv_offsets, kv_lens, return_lse=True)
+        ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets, kv_lens)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, *seg = ctx.saved_tensors
+        g = cross_attn_backward(dout.to(torch.bfloat16).contiguous(), q, k, v, out, lse, *seg)
+        return g["dq"], g["dk"], g["dv"], None, None, None
 
 
 def _host_tensor(t: torch.Tensor, name: str, dtype, shape):

@@ -192,6 +192,94 @@ moga_status check_window(int T, int Hg, int Wg, const int* window, int64_t* N) {
   return MOGA_OK;
 }
 
+// ------------------------------------------------------------------ query/key norm and rotation
+moga_status check_norm_side(const void* x, int64_t sn, int64_t sh, const float* w, moga_dtype dt, int64_t N, int H) {
+  const int64_t unit = dt == MOGA_BF16 ? 8 : 4;  // elements of a 16-byte access
+  if (N > 0 && !x) return MOGA_ERR_INVALID_ARG;
+  if (!aligned16(x) || (w && !aligned4(w))) return MOGA_ERR_INVALID_ARG;
+  if (sn < 0 || sh < 0) return MOGA_ERR_INVALID_ARG;
+  if ((N > 1 && sn % unit) || (H > 1 && sh % unit)) return MOGA_ERR_UNSUPPORTED;
+  return MOGA_OK;
+}
+
+// Checks what the two calls share and fills the arguments (outputs aside).
+moga_status norm_args(NormArgs* a, const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn,
+                      int64_t k_sh, moga_dtype dt, int64_t N, int H_q, int H_k, int d_h, const float* w_q,
+                      const float* w_k, float eps, const float* table, int P, const int* axes, const int* grid,
+                      int64_t token0, const int32_t* pos, int halves) {
+  if (dt != MOGA_F32 && dt != MOGA_BF16) return MOGA_ERR_INVALID_ARG;
+  if (N < 0 || N >= (int64_t)1 << 31 || H_q < 0 || H_k < 0 || H_q + (int64_t)H_k < 1) return MOGA_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || std::isinf(eps) || halves < 0 || halves > 1) return MOGA_ERR_INVALID_ARG;
+  if ((d_h != 64 && d_h != 128) || H_q > 65536 || H_k > 65536) return MOGA_ERR_UNSUPPORTED;
+  moga_status st;
+  if (H_q && (st = check_norm_side(q, q_sn, q_sh, w_q, dt, N, H_q)) != MOGA_OK) return st;
+  if (H_k && (st = check_norm_side(k, k_sn, k_sh, w_k, dt, N, H_k)) != MOGA_OK) return st;
+  a->x[0] = q, a->sn[0] = q_sn, a->sh[0] = q_sh, a->heads[0] = H_q, a->w[0] = w_q;
+  a->x[1] = k, a->sn[1] = k_sn, a->sh[1] = k_sh, a->heads[1] = H_k, a->w[1] = w_k;
+  a->N = N;
+  a->eps = eps;
+  if (!table) return pos || grid ? MOGA_ERR_INVALID_ARG : MOGA_OK;
+  if (!axes || axes[0] < 0 || axes[1] < 0 || axes[2] < 0 ||
+      (int64_t)axes[0] + axes[1] + axes[2] > d_h / 2 || P < 1 || (reinterpret_cast<uintptr_t>(table) & 7u))
+    return MOGA_ERR_INVALID_ARG;
+  a->table = table;
+  a->P = P;
+  a->end0 = axes[0];
+  a->end1 = a->end0 + axes[1];
+  a->end2 = a->end1 + axes[2];
+  if ((pos != nullptr) == (grid != nullptr)) return MOGA_ERR_INVALID_ARG;  // exactly one of them
+  if (pos) {
+    if (!aligned4(pos)) return MOGA_ERR_INVALID_ARG;
+    a->pos = pos;
+    return MOGA_OK;
+  }
+  if (grid[0] < 1 || grid[1] < 1 || grid[2] < 1) return MOGA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (axes[i] > 0 && grid[i] > P) return MOGA_ERR_INVALID_ARG;
+  const int64_t frame = (int64_t)grid[1] * grid[2];
+  if (frame >= (int64_t)1 << 31 || frame * grid[0] >= (int64_t)1 << 31) return MOGA_ERR_UNSUPPORTED;
+  if (token0 < 0 || token0 >= frame * grid[0]) return MOGA_ERR_INVALID_ARG;
+  a->token0 = (uint32_t)token0;
+  a->cells = (uint32_t)(frame * grid[0]);
+  a->frame = (uint32_t)frame;
+  a->width = (uint32_t)grid[2];
+  return MOGA_OK;
+}
+
+// ------------------------------------------------------------------ cross attention
+// Rows of n tokens x H heads at the given strides: token-major (a token's
+// heads inside its row) or head-major (whole token strides between heads).
+moga_status check_cross_rows(const void* x, int64_t sn, int64_t sh, int64_t n, int H, int d_h) {
+  if (n == 0) return MOGA_OK;
+  if (!x || !aligned16(x) || sn < 1 || sh < 1) return MOGA_ERR_INVALID_ARG;
+  if ((n > 1 && sn % 8) || (H > 1 && sh % 8)) return MOGA_ERR_UNSUPPORTED;
+  if (n > 1 && sn < d_h) return MOGA_ERR_UNSUPPORTED;
+  if (H > 1 && sh < d_h) return MOGA_ERR_UNSUPPORTED;
+  if (n > 1 && H > 1 && sn < (H - 1) * sh + d_h && (sh % sn || sh / sn < n)) return MOGA_ERR_UNSUPPORTED;
+  return MOGA_OK;
+}
+
+moga_status cross_args(CrossArgs* a, const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn,
+                       int64_t k_sh, const void* v, int64_t v_sn, int64_t v_sh, int64_t N, int64_t L, int H, int H_kv,
+                       int d_h, const int32_t* q_offsets, const int32_t* kv_offsets, const int32_t* kv_lens, int S) {
+  if (H_kv < 1 || H < 1 || H % H_kv) return MOGA_ERR_INVALID_ARG;
+  moga_status st;
+  if ((st = check_attn_shape(N, H, d_h)) != MOGA_OK || (st = check_attn_shape(L, H_kv, d_h)) != MOGA_OK) return st;
+  if (N >= (int64_t)1 << 30 || L >= (int64_t)1 << 30) return MOGA_ERR_UNSUPPORTED;
+  if (S < 1 || S > 1024 || (S > 1 && (!q_offsets || !kv_offsets))) return MOGA_ERR_INVALID_ARG;
+  if (!aligned4(q_offsets) || !aligned4(kv_offsets) || !aligned4(kv_lens)) return MOGA_ERR_INVALID_ARG;
+  if ((st = check_cross_rows(q, q_sn, q_sh, N, H, d_h)) != MOGA_OK ||
+      (st = check_cross_rows(k, k_sn, k_sh, L, H_kv, d_h)) != MOGA_OK ||
+      (st = check_cross_rows(v, v_sn, v_sh, L, H_kv, d_h)) != MOGA_OK)
+    return st;
+  a->q = q, a->q_sn = q_sn, a->q_sh = q_sh;
+  a->k = k, a->k_sn = k_sn, a->k_sh = k_sh;
+  a->v = v, a->v_sn = v_sn, a->v_sh = v_sh;
+  a->N = N, a->L = L, a->H = H, a->Hkv = H_kv, a->d_h = d_h;
+  a->q_off = q_offsets, a->kv_off = kv_offsets, a->kv_len = kv_lens, a->S = S;
+  return MOGA_OK;
+}
+
 // ------------------------------------------------------------------ bodies (args already validated)
 moga_status route_body(const DevCtx& c, const void* x, const void* W, const float* b, moga_dtype dt, int64_t N,
                        int d, int M, int32_t* gid, float* gate, int32_t* perm, int32_t* offsets,
@@ -1094,6 +1182,134 @@ moga_status moga_layer_ex(const void* x, const void* W_r, const float* b_r, moga
   if ((branches & 2) && (st = stga_body(c, q, k, v, T, Hg, Wg, frame_window, H, d_h, 1, out, w, scale)) != MOGA_OK)
     return st;
   return MOGA_OK;
+}
+
+moga_status moga_rope_table(int P, int d_h, const int* axes, double theta, float* table, void* stream) {
+  if (P < 1 || !axes || axes[0] < 0 || axes[1] < 0 || axes[2] < 0 || !(theta > 0.0) || std::isinf(theta) || !table ||
+      (reinterpret_cast<uintptr_t>(table) & 7u))
+    return MOGA_ERR_INVALID_ARG;
+  if (d_h != 64 && d_h != 128) return MOGA_ERR_UNSUPPORTED;
+  if ((int64_t)axes[0] + axes[1] + axes[2] > d_h / 2) return MOGA_ERR_INVALID_ARG;
+  DevCtx c;
+  if (!make_ctx(&c, nullptr, stream)) return MOGA_ERR_CUDA;
+  const moga_status st = from_cuda(launch_rope_table(c, P, d_h, axes, theta, table));
+  if (st == MOGA_OK) count(1);
+  return st;
+}
+
+size_t moga_qk_norm_rope_workspace_size(void) { return kHeader; }
+
+moga_status moga_qk_norm_rope(const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh,
+                              moga_dtype dt, int64_t N, int H_q, int H_k, int d_h, const float* w_q, const float* w_k,
+                              float eps, const float* table, int P, const int* axes, const int* grid, int64_t token0,
+                              const int32_t* pos, int halves, void* q_out, void* k_out, void* ws, size_t ws_bytes,
+                              void* stream) {
+  NormArgs a{};
+  const moga_status st = norm_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps, table, P,
+                                   axes, grid, token0, pos, halves);
+  if (st != MOGA_OK) return st;
+  if (N > 0 && ((H_q && !q_out) || (H_k && !k_out))) return MOGA_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(ws) || (pos && !ws)) return MOGA_ERR_INVALID_ARG;
+  if (ws && ws_bytes < kHeader) return MOGA_ERR_WORKSPACE;
+  DevCtx c;
+  if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  int launches = 0;
+  const cudaError_t e = launch_norm_rope(c, a, d_h, dt == MOGA_BF16, halves == 1, false, nullptr, nullptr, &launches);
+  count((uint64_t)launches);
+  return from_cuda(e);
+}
+
+size_t moga_qk_norm_rope_backward_workspace_size(int d_h) {
+  return d_h > 0 ? kHeader + (size_t)kNormBlocks * 2 * d_h * 4 : 0;
+}
+
+moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, int64_t q_sn,
+                                       int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh, moga_dtype dt,
+                                       int64_t N, int H_q, int H_k, int d_h, const float* w_q, const float* w_k,
+                                       float eps, const float* table, int P, const int* axes, const int* grid,
+                                       int64_t token0, const int32_t* pos, int halves, void* dq, void* dk,
+                                       float* dw_q, float* dw_k, void* ws, size_t ws_bytes, void* stream) {
+  NormArgs a{};
+  const moga_status st = norm_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps, table, P,
+                                   axes, grid, token0, pos, halves);
+  if (st != MOGA_OK) return st;
+  if (N > 0 && ((H_q && (!dq_out || !dq)) || (H_k && (!dk_out || !dk)))) return MOGA_ERR_INVALID_ARG;
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned4(dw_q) ||
+      !aligned4(dw_k) || !ws || !aligned16(ws))
+    return MOGA_ERR_INVALID_ARG;
+  if (ws_bytes < moga_qk_norm_rope_backward_workspace_size(d_h)) return MOGA_ERR_WORKSPACE;
+  DevCtx c;
+  if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
+  a.dy[0] = dq_out;
+  a.dy[1] = dk_out;
+  a.y[0] = dq;
+  a.y[1] = dk;
+  a.part = reinterpret_cast<float*>((uint8_t*)ws + kHeader);
+  int launches = 0;
+  const cudaError_t e = launch_norm_rope(c, a, d_h, dt == MOGA_BF16, halves == 1, true, dw_q, dw_k, &launches);
+  count((uint64_t)launches);
+  return from_cuda(e);
+}
+
+size_t moga_cross_attn_workspace_size(int64_t N, int64_t L, int H, int H_kv, int d_h, int S) {
+  if (N < 0 || L < 0 || H < 1 || H_kv < 1 || d_h < 1 || S < 1) return 0;
+  return kHeader + cross_fwd_ws_bytes(N, L, H, H_kv, d_h, S);
+}
+
+moga_status moga_cross_attn(const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh,
+                            const void* v, int64_t v_sn, int64_t v_sh, int64_t N, int64_t L, int H, int H_kv, int d_h,
+                            const int32_t* q_offsets, const int32_t* kv_offsets, const int32_t* kv_lens, int S,
+                            void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  CrossArgs a{};
+  const moga_status st = cross_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, v, v_sn, v_sh, N, L, H, H_kv, d_h, q_offsets,
+                                    kv_offsets, kv_lens, S);
+  if (st != MOGA_OK) return st;
+  if ((N > 0 && !out) || !aligned16(out) || !aligned4(lse) || !ws || !aligned16(ws)) return MOGA_ERR_INVALID_ARG;
+  if (ws_bytes < moga_cross_attn_workspace_size(N, L, H, H_kv, d_h, S)) return MOGA_ERR_WORKSPACE;
+  DevCtx c;
+  if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
+  a.out = out;
+  a.lse = lse;
+  int launches = 0;
+  const cudaError_t e = launch_cross_attn(c, a, (uint8_t*)ws + kHeader, &launches);
+  count((uint64_t)launches);
+  return from_cuda(e);
+}
+
+size_t moga_cross_attn_backward_workspace_size(int64_t N, int64_t L, int H, int H_kv, int d_h, int S) {
+  if (N < 0 || L < 0 || H < 1 || H_kv < 1 || d_h < 1 || S < 1) return 0;
+  return kHeader + cross_bwd_ws_bytes(N, L, H, H_kv, d_h, S);
+}
+
+moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_sn, int64_t q_sh, const void* k,
+                                     int64_t k_sn, int64_t k_sh, const void* v, int64_t v_sn, int64_t v_sh, int64_t N,
+                                     int64_t L, int H, int H_kv, int d_h, const int32_t* q_offsets,
+                                     const int32_t* kv_offsets, const int32_t* kv_lens, int S, const void* out,
+                                     const float* lse, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  CrossArgs a{};
+  const moga_status st = cross_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, v, v_sn, v_sh, N, L, H, H_kv, d_h, q_offsets,
+                                    kv_offsets, kv_lens, S);
+  if (st != MOGA_OK) return st;
+  if ((N > 0 && (!dout || !out || !lse || !dq)) || (L > 0 && (!dk || !dv))) return MOGA_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(out) || !aligned4(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      !ws || !aligned16(ws))
+    return MOGA_ERR_INVALID_ARG;
+  if (ws_bytes < moga_cross_attn_backward_workspace_size(N, L, H, H_kv, d_h, S)) return MOGA_ERR_WORKSPACE;
+  DevCtx c;
+  if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
+  a.out = const_cast<void*>(out);
+  a.lse = const_cast<float*>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  int launches = 0;
+  const cudaError_t e = launch_cross_bwd(c, a, (uint8_t*)ws + kHeader, &launches);
+  count((uint64_t)launches);
+  return from_cuda(e);
 }
 
 moga_status moga_route_noalloc_status(void* stream) {

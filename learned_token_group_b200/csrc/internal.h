@@ -150,6 +150,56 @@ cudaError_t launch_route_bwd(const DevCtx& c, const void* x, const void* W, cons
                              int d, int M, const int32_t* gid, const float* dgate, const int32_t* offsets,
                              float balance_alpha, void* dx, float* dW, float* db, uint8_t* ws);
 
+// ------------------------------------------------------------------ query/key norm and rotation (norm.cu)
+constexpr int kNormBlocks = 1024;  // upper bound on blocks, each with its partial sums of dw
+struct NormArgs {
+  // [0] queries, [1] keys
+  const void* x[2];
+  int64_t sn[2], sh[2];  // token and head strides of x, in elements
+  int heads[2];
+  const float* w[2];     // [d_h], or null (1)
+  const void* dy[2];     // backward: bf16 [N, heads, d_h]
+  void* y[2];            // forward: bf16 [N, heads, d_h]; backward: dx in x's dtype, [N, heads, d_h]
+  float* part;           // backward: [blocks][2][d_h] partial sums of dw
+  int64_t N;
+  float eps;
+  // rotation: pairs [0, end0) turn with axis 0, [end0, end1) with axis 1,
+  // [end1, end2) with axis 2; end2 = 0: no rotation
+  const float* table;    // (cos, sin) [P][half]
+  int P, half, end0, end1, end2;
+  const int32_t* pos;    // [N][3], or null: the place of token (token0 + n) mod cells on the grid
+  uint32_t token0, cells, frame, width;
+  int chunks[2], rows[2];  // set by the launcher
+};
+cudaError_t launch_rope_table(const DevCtx& c, int P, int d_h, const int* axes, double theta, float* table);
+cudaError_t launch_norm_rope(const DevCtx& c, NormArgs a, int d_h, bool bf16, bool halves, bool backward,
+                             float* dwq, float* dwk, int* launches);
+
+// ------------------------------------------------------------------ cross attention (cross.cu)
+struct CrossArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_sn, q_sh, k_sn, k_sh, v_sn, v_sh;  // token and head strides, in elements
+  int64_t N, L;
+  int H, Hkv, d_h;
+  const int32_t* q_off;   // [S + 1], or null with one segment: all rows
+  const int32_t* kv_off;  // [S + 1], or null with one segment: all rows
+  const int32_t* kv_len;  // [S], or null: up to the next offset
+  int S;
+  void* out;              // bf16 [N, H, d_h] (backward: read)
+  float* lse;             // fp32 [H, N], nullable in the forward (backward: read)
+  const void* dout;       // backward: bf16 [N, H, d_h]
+  void* dq;               // bf16 [N, H, d_h]
+  void* dk;               // bf16 [L, H_kv, d_h]
+  void* dv;
+  float* dsum;            // [H, N]
+};
+size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
+size_t cross_bwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
+cudaError_t launch_cross_attn(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches);
+cudaError_t launch_cross_bwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches);
+
 // ------------------------------------------------------------------ shot windows
 // Window table of shot-aware STGA (int32, device):
 //   [0] windows, [1] work units (query-tile pairs x heads), [2] key/value rows, [3] spare,

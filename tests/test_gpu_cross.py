@@ -1,0 +1,443 @@
+"""Cross attention and its gradients on the GPU against the oracle (float64).
+
+Tolerances, elementwise, for inputs given in bf16:
+* a score is a sum of d_h exact products in fp32: off by at most
+  delta = d_h 2^-23 max_ij sum_c |q_ic k_jc| / sqrt(d_h), and so, relatively,
+  is exp(score); exp2 and its argument's rounding add under 2^-14.
+* out: rounded once (2^-8 |out|); P enters the product as bf16 (2^-8); so
+  2^-8 |out| + (2^-8 + 2^-12 + 2 delta) sum_j p_ij |v_j|.
+* lse: delta, the sum's roundings (under 2^-16) and its own (2^-22 |lse|).
+* dv: as out, with dO for v.
+* dq, dk: rounded once; dS enters as bf16 (2^-8) and sums of some thousand
+  terms in fp32 (2^-11); D comes from out rounded to bf16 (2^-8 of sum_c
+  |dO_c O_c|); P = exp(S - lse) carries 2 delta + 2^-14; dP and D carry
+  eta = d_h 2^-23 max sum_c |dO_c v_c| each.
+* fp32 holds no normal number below 2^-126: a P under that may be 0.  Such an
+  error reaches a sum at most 2^-126 x 2^11 rows x 2^12 (|dP| |Q| at most, here)
+  < 2^-100 (TINY), which every tolerance includes.
+"""
+import numpy as np
+import pytest
+import torch
+
+import learned_token_group_b200 as moga
+import oracle
+from oracle import around
+from parity import np_cpu
+
+pytestmark = pytest.mark.gpu
+
+B = 2.0 ** -8
+TINY = 2.0 ** -100
+TIMEOUT, DEVICE_CHECK = 5, 6
+
+
+def rnd(g, *s):
+    return torch.randn(s, generator=g, device="cuda")
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def layout_of(x, how):
+    """x [n, h, d] with the same values in other memory."""
+    n, h, d = x.shape
+    if how == "packed":                               # beside another tensor of the same rows
+        return torch.cat([x, torch.full_like(x, float("nan"))], 1)[:, :h]
+    if how == "head_major":
+        return x.transpose(0, 1).contiguous().transpose(0, 1)
+    if how == "head_rows":                            # head-major with rows to spare
+        y = torch.full((h, n + 5, d), float("nan"), dtype=x.dtype, device=x.device)
+        y[:, :n] = x.transpose(0, 1)
+        return y[:, :n].transpose(0, 1)
+    if how == "wide":                                 # a token stride that is no multiple of the head's
+        y = torch.full((n, h * d + 24), float("nan"), dtype=x.dtype, device=x.device)
+        y[:, :h * d] = x.reshape(n, h * d)
+        return y.as_strided((n, h, d), (h * d + 24, d, 1))
+    return x
+
+
+class Case:
+    def __init__(self, q_lens, k_lens, H, Hk, d, seed=0, layout="dense", padded=False, edge=0, peak=1.0, poison=True):
+        """Segments of q_lens queries and k_lens keys; padded: each segment's
+        keys in a place of the longest's size; edge: rows before the first and
+        behind the last segment.  Whatever belongs to no segment is NaN."""
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        S = len(q_lens)
+        qo = edge + np.concatenate([[0], np.cumsum(q_lens)])
+        width = [max(k_lens)] * S if padded else k_lens
+        ko = edge + np.concatenate([[0], np.cumsum(width)])
+        N, L = int(qo[-1]) + edge, int(ko[-1]) + edge
+        self.N, self.L, self.H, self.Hk, self.d = N, L, H, Hk, d
+        q, k, v, dout = (rnd(g, n, h, d) for n, h in ((N, H), (L, Hk), (L, Hk), (N, H)))
+        q = 1.3 * peak * q
+        if peak > 1 and L:                            # some keys that queries match
+            k[:min(N, L)] = peak * q[:min(N, L), ::H // Hk] / (1.3 * peak)
+        self.seg = [(int(qo[s]), int(qo[s + 1]), int(ko[s]), int(ko[s]) + int(k_lens[s])) for s in range(S)]
+        if poison:
+            for t, (a, b) in ((q, (0, 1)), (k, (2, 3)), (v, (2, 3)), (dout, (0, 1))):
+                dead = torch.ones(len(t), dtype=torch.bool, device="cuda")
+                for s in self.seg:
+                    dead[s[a]:s[b]] = False
+                t[dead] = float("nan")
+        self.q, self.k, self.v, self.dout = (t.to(torch.bfloat16) for t in (q, k, v, dout))
+        whole = S == 1 and not edge
+        self.seg_args = dict(q_offsets=None if whole else ints(qo), kv_offsets=None if whole else ints(ko),
+                             kv_lens=ints(k_lens) if padded else None)
+        self.in_place = [layout_of(t, layout) for t in (self.q, self.k, self.v)]
+
+    def reference(self, dout=None):
+        r = around.cross(self.q, self.k, self.v, self.seg, dout)
+        sc = 1 / np.sqrt(self.d)
+        f = lambda t: np.abs(around.f64(t))  # noqa: E731
+        self.delta = self.eta = 0.0
+        for q0, q1, k0, k1 in self.seg:
+            if q1 > q0 and k1 > k0:
+                for h in range(self.H):
+                    kh = h // (self.H // self.Hk)
+                    self.delta = max(self.delta, self.d * 2.0 ** -23 * sc * (f(self.q[q0:q1, h]) @ f(self.k[k0:k1, kh]).T).max())
+                    if dout is not None:
+                        self.eta = max(self.eta, self.d * 2.0 ** -23 * (f(dout[q0:q1, h]) @ f(self.v[k0:k1, kh]).T).max())
+        return r
+
+
+def near(got, want, tol, what=""):
+    a = np_cpu(got).astype(np.float64)
+    inside = ~np.isnan(want)
+    a, want, tol = a[inside], want[inside], tol[inside]
+    assert np.isfinite(a).all(), f"{what}: not finite"
+    over = np.abs(a - want) - tol - TINY
+    assert a.size == 0 or over.max() <= 0, f"{what}: off by {np.abs(a - want).max():.3e}, {over.max():.3e} over"
+
+
+def check_forward(c, **kw):
+    r = c.reference()
+    out, lse = moga.cross_attn(*c.in_place, **c.seg_args, return_lse=True, **kw)
+    near(out, r["out"], B * np.abs(r["out"]) + (B + 2.0 ** -12 + 2 * c.delta) * r["out_size"], what="out")
+    got = np_cpu(lse)
+    keys = np.isfinite(r["lse"])
+    assert np.isneginf(got[np.isneginf(r["lse"])]).all()
+    assert (np.abs(got[keys] - r["lse"][keys]) <= c.delta + 2.0 ** -16 + 2.0 ** -22 * np.abs(r["lse"][keys])).all()
+    outside = np.isnan(r["out"][:, 0, 0]) if c.N else np.zeros(0, bool)
+    assert (np_cpu(out)[outside] == 0).all() and np.isneginf(got[:, outside]).all()
+    assert torch.equal(out, moga.cross_attn(*c.in_place, **c.seg_args))       # the same without lse, and again
+    return out, lse
+
+
+def check_backward(c, out, lse, **kw):
+    r = c.reference(c.dout)
+    g = moga.cross_attn_backward(c.dout, *c.in_place, out, lse, **c.seg_args, **kw)
+    moga.sync_status(g["ws"])
+    for n in ("dq", "dk"):
+        near(g[n], r[n], B * np.abs(r[n]) + (B + 2.0 ** -11) * r[n + "_size"] + B * r[n + "_d"] +
+             (2 * c.delta + 2.0 ** -14) * r[n + "_p"] + 2 * c.eta * r[n + "_1"], what=n)
+    near(g["dv"], r["dv"], B * np.abs(r["dv"]) + (B + 2.0 ** -11 + 2 * c.delta) * r["dv_size"], what="dv")
+    for n in ("dq", "dk", "dv"):
+        assert (np_cpu(g[n])[np.isnan(r["dv" if n == "dv" else n])] == 0).all()
+    return g
+
+
+def check(*a, **kw):
+    c = Case(*a, **kw)
+    out, lse = check_forward(c)
+    check_backward(c, out, lse)
+    return c
+
+
+ONE = [(1, 1, 1, 1, 128), (1, 77, 12, 12, 128), (1, 16, 2, 2, 64), (5, 128, 2, 1, 128), (128, 129, 1, 1, 64),
+       (129, 127, 2, 2, 128), (257, 300, 3, 1, 128), (300, 512, 2, 2, 64), (130, 1, 2, 2, 128), (3, 2000, 2, 2, 128),
+       (700, 1030, 4, 2, 64), (256, 256, 1, 1, 128), (77, 5003, 3, 3, 128), (1500, 77, 8, 1, 64), (2, 15, 1, 1, 128),
+       (385, 640, 1, 1, 128), (64, 3000, 16, 4, 64)]
+
+
+@pytest.mark.parametrize("N,L,H,Hk,d", ONE)
+def test_one_segment(N, L, H, Hk, d):
+    check([N], [L], H, Hk, d, seed=N + L)
+
+
+SEGS = {
+    "ragged": ([130, 0, 1, 300, 7, 256], [5, 64, 0, 257, 128, 33]),
+    "singles": ([1] * 9, [1, 2, 0, 128, 129, 300, 17, 0, 64]),
+    "empty": ([3, 0, 5], [0, 0, 0]),
+    "many": (list(range(40)), [(7 * i) % 150 for i in range(40)]),
+    "long_short": ([1000, 1], [3, 1500]),
+}
+
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("edge", [0, 3])
+@pytest.mark.parametrize("d,H,Hk", [(128, 2, 2), (64, 4, 1)])
+@pytest.mark.parametrize("name", sorted(SEGS))
+def test_segments(name, d, H, Hk, edge, padded):
+    check(*SEGS[name], H, Hk, d, seed=edge, edge=edge, padded=padded)
+
+
+@pytest.mark.parametrize("layout", ["packed", "head_major", "head_rows", "wide"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_layouts(layout, d):
+    check([140, 200], [70, 150], 4, 2, d, layout=layout)
+    check([150], [200], 1, 1, d, layout=layout)
+    check([1], [200], 3, 3, d, layout=layout)
+
+
+@pytest.mark.parametrize("peak", [2.0, 6.0])
+def test_matched_keys(peak):
+    """A query's own key takes nearly all of its row, and running maxima grow from tile to tile."""
+    check([300], [700], 2, 2, 128, peak=peak)
+    check([2], [3000], 2, 2, 64, peak=peak)
+
+
+def test_growing_scores():
+    """Keys sorted by their score: every tile's maximum is above the last one's by more than 2^8."""
+    c = Case([200], [900], 1, 1, 128)
+    u = torch.zeros(128, device="cuda")
+    u[0] = 1
+    c.q = (c.q.float() * 0.1 + 8 * u).to(torch.bfloat16)
+    c.k = (c.k.float() * 0.1 + torch.linspace(-40, 40, 900, device="cuda")[:, None, None] * u).to(torch.bfloat16)
+    c.in_place = [c.q, c.k, c.v]
+    check_backward(c, *check_forward(c))
+
+
+def test_no_rows():
+    q, k = (torch.zeros(n, 2, 128, dtype=torch.bfloat16, device="cuda") for n in (0, 5))
+    out, lse = moga.cross_attn(q, k, k, return_lse=True)
+    assert out.shape == (0, 2, 128) and lse.shape == (2, 0)
+    g = moga.cross_attn_backward(q, q, k, k, out, lse)
+    assert (g["dk"] == 0).all() and (g["dv"] == 0).all() and g["dq"].shape == (0, 2, 128)
+    out, lse = moga.cross_attn(k, q, q, return_lse=True)              # queries, no keys
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    g = moga.cross_attn_backward(k, k, q, q, out, lse)
+    assert (g["dq"] == 0).all() and g["dk"].shape == (0, 2, 128)
+
+
+def test_rows_of_no_segment_are_left_as_they_were():
+    c = Case([100, 30], [40, 0], 2, 2, 128, edge=4)
+    out = torch.full((c.N, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert moga.cross_attn(*c.in_place, **c.seg_args, out=out) is out
+    assert (out[:4] == 7).all() and (out[134:] == 7).all() and (out[104:134] == 0).all()
+
+
+BAD = [dict(q_offsets=[0, 60, 50]), dict(q_offsets=[-1, 50, 100]), dict(q_offsets=[0, 50, 101]),
+       dict(kv_offsets=[0, 60, 50]), dict(kv_offsets=[-2, 50, 80]), dict(kv_offsets=[0, 50, 81]),
+       dict(kv_lens=[41, 3]), dict(kv_lens=[3, -1]), dict(kv_offsets=[0, 2 ** 31 - 1, 80]),
+       dict(kv_lens=[2 ** 31 - 1, 3])]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=[str(b) for b in BAD])
+def test_bad_segments_are_reported_and_nothing_is_written(bad):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    q, k, v = (rnd(g, n, 2, 64).to(torch.bfloat16) for n in (100, 80, 80))
+    seg = dict(q_offsets=[0, 50, 100], kv_offsets=[0, 40, 80], kv_lens=[40, 40])
+    good = {n: ints(x) for n, x in seg.items()}
+    broken = {n: ints(x) for n, x in dict(seg, **bad).items()}
+    ws = moga.workspace(moga.cross_attn_workspace_size(q, k, 2, backward=True), "cuda")
+    out = torch.full((100, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    moga.cross_attn(q, k, v, **broken, out=out, ws=ws)
+    with pytest.raises(moga.MogaError) as e:
+        moga.sync_status(ws)
+    assert e.value.status == DEVICE_CHECK and (out == 7).all()
+    out, lse = moga.cross_attn(q, k, v, **good, return_lse=True, ws=ws)
+    moga.sync_status(ws)
+    gr = moga.cross_attn_backward(q, q, k, v, out, lse, **broken, ws=ws)
+    with pytest.raises(moga.MogaError):
+        moga.sync_status(ws)
+    assert all((gr[n] == 0).all() for n in ("dq", "dk", "dv"))
+    moga.cross_attn_backward(q, q, k, v, out, lse, **good, ws=ws)
+    moga.sync_status(ws)
+
+
+def test_the_same_bits_again_with_a_used_workspace():
+    """Calls of other sizes in between leave nothing behind; sums are taken in a fixed order."""
+    cs = [Case([700], [300], 4, 2, 128), Case([3], [4000], 2, 2, 64), Case(*SEGS["ragged"], 4, 4, 128)]
+    ws = moga.workspace(max(moga.cross_attn_workspace_size(c.q, c.k, len(c.seg), True) for c in cs), "cuda")
+    runs = []
+    for _ in range(2):
+        for c in cs:
+            out, lse = moga.cross_attn(*c.in_place, **c.seg_args, return_lse=True, ws=ws)
+            g = moga.cross_attn_backward(c.dout, *c.in_place, out, lse, **c.seg_args, ws=ws)
+            runs.append((out, lse, g["dq"], g["dk"], g["dv"]))
+    moga.sync_status(ws)
+    for a, b in zip(runs[:3], runs[3:]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_other_streams_and_replayed_graphs():
+    cs = [Case([500], [300], 2, 2, 128, seed=1), Case([4], [3000], 2, 2, 128, seed=2)]
+    ws = moga.workspace(max(moga.cross_attn_workspace_size(c.q, c.k, 1, True) for c in cs), "cuda")
+
+    def step(c, ws=None):
+        out, lse = moga.cross_attn(*c.in_place, return_lse=True, ws=ws)
+        g = moga.cross_attn_backward(c.dout, *c.in_place, out, lse, ws=ws)
+        return out, lse, g["dq"], g["dk"], g["dv"]
+    want = [step(c) for c in cs]
+    torch.cuda.synchronize()
+    got = []
+    for c in cs:                                      # at once, each with its own workspace
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got.append(step(c))
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    graphs = []
+    for c in cs:                                      # two graphs of one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, step(c, ws)))
+    old = [c.v.clone() for c in cs]
+    for f in (2.0, 1.0):
+        for c, v in zip(cs, old):
+            c.v.copy_(v * f)
+        for g, _ in graphs * 2:
+            g.replay()
+        torch.cuda.synchronize()
+        now = [step(c) for c in cs]
+        for (_, a), b in zip(graphs, now):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    moga.sync_status(ws)
+
+
+@pytest.mark.parametrize("layout", ["dense", "views", "broadcast"])
+def test_autograd(layout):
+    """The function's gradients against 64-bit autograd of the formula."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    q = rnd(g, 120, 4, 72).to(torch.bfloat16).requires_grad_()
+    kv = rnd(g, 90, 2, 2, 72).to(torch.bfloat16).requires_grad_()
+    co = rnd(g, 120, 4, 64).to(torch.bfloat16)
+    if layout == "views":                             # heads off a 16-byte boundary, keys and values side by side
+        view = lambda q, kv: (q[..., 3:67], kv[:, 0, :, :64], kv[:, 1, :, :64])  # noqa: E731
+    elif layout == "broadcast":                       # one key head for all, one value row for all
+        view = lambda q, kv: (q[..., :64], kv[:, 0, :1, :64].expand(90, 4, 64), kv[:1, 1, :1, :64].expand(90, 4, 64))  # noqa: E731
+    else:
+        view = lambda q, kv: (q[..., :64].contiguous(), kv[:, 0, :, :64].contiguous(), kv[:, 1, :, :64].contiguous())  # noqa: E731
+    qo, ko = [0, 50, 120], [0, 60, 90]
+    out = moga.CrossAttnFunction.apply(*view(q, kv), ints(qo), ints(ko))
+    (out * co).float().sum().backward()
+    q64, kv64 = (t.detach().double().requires_grad_() for t in (q, kv))
+    a, b, c = view(q64, kv64)
+    loss = 0
+    for (q0, q1), (k0, k1) in zip(zip(qo, qo[1:]), zip(ko, ko[1:])):
+        for h in range(4):
+            kh = h * b.shape[1] // 4
+            p = torch.softmax(a[q0:q1, h] @ b[k0:k1, kh].t() / 8, -1)
+            loss = loss + ((p @ c[k0:k1, kh]) * co[q0:q1, h].double()).sum()
+    loss.backward()
+    # each gradient is rounded once and made of products with P or dS rounded once (their errors spread over the
+    # sum); a broadcast adds its terms in bf16: 2^-8 of the largest each, at most 4 of them.  One value row for all
+    # keys makes dq 0, and the reference itself is then off by its 64-bit roundings: 2^-53 of some 2^7 terms of at
+    # most 2^6 each, under 2^-40
+    for x, y in ((q.grad, q64.grad), (kv.grad, kv64.grad)):
+        off, most = (x.double() - y).abs().max().item(), y.abs().max().item()
+        assert off <= 4 * B * most + 2.0 ** -40
+
+
+def test_refusals():
+    q, k = (torch.zeros(n, h, 64, dtype=torch.bfloat16, device="cuda") for n, h in ((10, 4), (8, 2)))
+
+    def no(match, *a, **kw):
+        with pytest.raises((ValueError, moga.MogaError), match=match):
+            moga.cross_attn(*a, **kw)
+    no("bfloat16", q.float(), k, k)
+    no("k and v must be", q, k, k[:5])
+    no("k and v must be", q[:, :3], k, k)
+    no("tokens, heads", q[0], k, k)
+    no("dense", q[..., ::2], k, k)
+    no("UNSUPPORTED", q[..., :32], k[..., :32], k[..., :32])
+    no("several segments", q, k, k, q_offsets=ints([0, 5, 10]))
+    no("_offsets must be", q, k, k, q_offsets=ints([0, 5, 10]), kv_offsets=ints([0, 8]))
+    no("int32", q, k, k, q_offsets=ints([0]), kv_offsets=ints([0]))
+    no("q_offsets", q, k, k, q_offsets=ints([0, 5, 10]).long(), kv_offsets=ints([0, 3, 8]))
+    no("kv_lens", q, k, k, kv_lens=ints([1, 2]))
+    no("out", q, k, k, out=torch.zeros(10, 4, 64, device="cuda"))
+    no("must be on", q, k, k, kv_lens=torch.zeros(1, dtype=torch.int32))
+    no("WORKSPACE", q, k, k, ws=moga.workspace(256, "cuda")[:128])
+    no("INVALID_ARG", q, k[:, :1].expand(8, 2, 64), k)  # a head stride of zero: autograd's function copies it
+    out, lse = moga.cross_attn(q, k, k, return_lse=True)
+    for kw in (dict(dout=q.float()), dict(out=out[:5]), dict(lse=lse.t()), dict(lse=lse.double())):
+        with pytest.raises(ValueError):
+            moga.cross_attn_backward(**dict(dict(dout=q, q=q, k=k, v=k, out=out, lse=lse), **kw))
+
+
+def test_block_with_its_text_attention():
+    """As used: norm and rotation, the visual block, then attention to each shot's prompt; against the oracle."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    grid, N, H, d, M = (3, 10, 12), 360, 2, 128, 3
+    qkv = rnd(g, N, 3 * H, d).to(torch.bfloat16)
+    w = [1 + 0.2 * rnd(g, d) for _ in range(4)]
+    x, W_r = rnd(g, N, 64).to(torch.bfloat16), (rnd(g, M, 64) / 8).to(torch.bfloat16)
+    axes = (24, 20, 20)
+    table = moga.rope_table(12, d, axes)
+    q, k = moga.qk_norm_rope(qkv[:, :H], qkv[:, H:2 * H], w[0], w[1], table, axes, grid)
+    v = qkv[:, 2 * H:].contiguous()
+    res = moga.moga_layer(x, W_r, None, q, k, v, M, grid, (3, 8, 8))
+    text = rnd(g, 50, 2, H, d).to(torch.bfloat16)
+    q2, _ = moga.qk_norm_rope(res["out"], None, w[2], None)
+    _, k2 = moga.qk_norm_rope(None, text[:, 0], None, w[3])
+    qo, ko = [0, 120, 360], [0, 27, 50]
+    ws = moga.workspace(moga.cross_attn_workspace_size(q2, k2, 2), "cuda")
+    out = moga.cross_attn(q2, k2, text[:, 1], ints(qo), ints(ko), ws=ws)
+    moga.sync_status(res["ws"])
+    moga.sync_status(ws)
+    # the oracle, step by step from the GPU's own inputs of each step (their roundings are tested above)
+    ang = around.angles(around.grid_positions(N, grid), axes, d)
+    for got, xi, wi in ((q, qkv[:, :H], w[0]), (k, qkv[:, H:2 * H], w[1])):
+        want, size = around.norm_rope(xi, wi, 1e-6, ang, False)
+        assert (np.abs(np_cpu(got) - want) <= B * np.abs(want) * 1.001 + 2.0 ** -19 * size).all()
+    f = lambda t: np_cpu(t).astype(np.float64)  # noqa: E731
+    ref = oracle.moga_layer(f(x), f(W_r), None, f(q), f(k), f(v), M, grid=grid, window=(3, 8, 8))
+    assert np.abs(f(res["out"]) - ref["out"]).max() <= 2e-2
+    want = around.cross(q2, k2, text[:, 1], [(0, 120, 0, 27), (120, 360, 27, 50)])
+    assert (np.abs(f(out) - want["out"]) <= B * np.abs(want["out"]) + (B + 2.0 ** -11) * want["out_size"]).all()
+
+
+def test_training_step_through_block_and_text_attention():
+    """The three autograd functions in a row; each one's gradients are those of its own backward call."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    grid, N, H, d, M = (2, 10, 12), 240, 2, 64, 3
+    qkv = rnd(g, N, 3 * H, d).to(torch.bfloat16).requires_grad_()
+    text = rnd(g, 40, 2, H, d).to(torch.bfloat16).requires_grad_()
+    w = [(1 + 0.2 * rnd(g, d)).requires_grad_() for _ in range(4)]
+    x, W_r = (t.to(torch.bfloat16).requires_grad_() for t in (rnd(g, N, 64), rnd(g, M, 64) / 8))
+    axes, table = (12, 10, 10), moga.rope_table(12, d, (12, 10, 10))
+    qo, ko = ints([0, 120, 240]), ints([0, 25, 40])
+    norm, block, cross = moga.QkNormRopeFunction.apply, moga.MogaFunction.apply, moga.CrossAttnFunction.apply
+    q, k = norm(qkv[:, :H], qkv[:, H:2 * H], w[0], w[1], table, axes, grid)
+    y = block(x, W_r, None, q, k, qkv[:, 2 * H:], M, grid, (2, 8, 8))
+    q2, _ = norm(y, None, w[2])
+    _, k2 = norm(None, text[:, 0], None, w[3])
+    out = cross(q2, k2, text[:, 1], qo, ko)
+    dout = rnd(g, N, H, d).to(torch.bfloat16)
+    mid = torch.autograd.grad(out, [q2, k2, y, q, k], dout, retain_graph=True)
+    out.backward(dout)
+    with torch.no_grad():
+        o, lse = moga.cross_attn(q2, k2, text[:, 1], qo, ko, return_lse=True)
+        gc = moga.cross_attn_backward(dout, q2, k2, text[:, 1], o, lse, qo, ko)
+        assert torch.equal(gc["dq"], mid[0]) and torch.equal(gc["dk"], mid[1])
+        assert torch.equal(text.grad[:, 1], gc["dv"])
+        g2 = moga.qk_norm_rope_backward(mid[0], None, y, None, w[2])
+        assert torch.equal(g2["dq"], mid[2]) and torch.equal(g2["dw_q"], w[2].grad)
+        g1 = moga.qk_norm_rope_backward(mid[3], mid[4], qkv[:, :H], qkv[:, H:2 * H], w[0], w[1], table, axes, grid)
+        assert torch.equal(g1["dq"], qkv.grad[:, :H]) and torch.equal(g1["dk"], qkv.grad[:, H:2 * H])
+        assert torch.equal(g1["dw_q"], w[0].grad)
+    for t in (x, W_r, qkv, text, *w):
+        assert torch.isfinite(t.grad).all() and t.grad.abs().max() > 0
+
+
+def test_offsets_past_32_bits():
+    """Keys that start past 2^31 elements of one buffer (4 GB, mostly untouched)."""
+    L, d = 300, 128
+    sn = (1 << 31) // 256 + 128
+    buf = torch.empty((L - 1) * sn + 2 * d, dtype=torch.bfloat16, device="cuda")
+    k = buf.as_strided((L, 2, d), (sn, d, 1))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    c = Case([40], [L], 2, 2, d)
+    k.copy_(c.k)
+    c.in_place[1] = k
+    check_backward(c, *check_forward(c))
