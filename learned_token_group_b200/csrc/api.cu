@@ -249,14 +249,19 @@ moga_status norm_args(NormArgs* a, const void* q, int64_t q_sn, int64_t q_sh, co
 // ------------------------------------------------------------------ cross attention
 // Rows of n tokens x H heads at the given strides: token-major (a token's
 // heads inside its row) or head-major (whole token strides between heads).
-moga_status check_cross_rows(const void* x, int64_t sn, int64_t sh, int64_t n, int H, int d_h) {
+// The stride of a dimension of one element says nothing: it is set to what a
+// dense tensor has.
+moga_status check_cross_rows(const void* x, int64_t* sn, int64_t* sh, int64_t n, int H, int d_h) {
   if (n == 0) return MOGA_OK;
-  if (!x || !aligned16(x) || sn < 1 || sh < 1) return MOGA_ERR_INVALID_ARG;
-  if ((n > 1 && sn % 8) || (H > 1 && sh % 8)) return MOGA_ERR_UNSUPPORTED;
-  if (n > 1 && sn < d_h) return MOGA_ERR_UNSUPPORTED;
-  if (H > 1 && sh < d_h) return MOGA_ERR_UNSUPPORTED;
-  if (n > 1 && H > 1 && sn < (H - 1) * sh + d_h && (sh % sn || sh / sn < n)) return MOGA_ERR_UNSUPPORTED;
-  return MOGA_OK;
+  if (!x || !aligned16(x) || *sn < 1 || *sh < 1) return MOGA_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 31;  // coordinates of a tensor map
+  if (*sn >= (int64_t)1 << 38 || *sh >= (int64_t)1 << 38) return MOGA_ERR_UNSUPPORTED;
+  if (H == 1) *sh = d_h;
+  if (n == 1) *sn = H * *sh;
+  if (*sn % 8 || *sh % 8 || *sn < d_h || *sh < d_h) return MOGA_ERR_UNSUPPORTED;
+  if (*sn >= (H - 1) * *sh + d_h) return (H - 1) * *sh + d_h < most ? MOGA_OK : MOGA_ERR_UNSUPPORTED;
+  if (*sh % *sn || *sh / *sn < n) return MOGA_ERR_UNSUPPORTED;
+  return (H - 1) * (*sh / *sn) + n < most ? MOGA_OK : MOGA_ERR_UNSUPPORTED;
 }
 
 moga_status cross_args(CrossArgs* a, const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn,
@@ -268,9 +273,9 @@ moga_status cross_args(CrossArgs* a, const void* q, int64_t q_sn, int64_t q_sh, 
   if (N >= (int64_t)1 << 30 || L >= (int64_t)1 << 30) return MOGA_ERR_UNSUPPORTED;
   if (S < 1 || S > 1024 || (S > 1 && (!q_offsets || !kv_offsets))) return MOGA_ERR_INVALID_ARG;
   if (!aligned4(q_offsets) || !aligned4(kv_offsets) || !aligned4(kv_lens)) return MOGA_ERR_INVALID_ARG;
-  if ((st = check_cross_rows(q, q_sn, q_sh, N, H, d_h)) != MOGA_OK ||
-      (st = check_cross_rows(k, k_sn, k_sh, L, H_kv, d_h)) != MOGA_OK ||
-      (st = check_cross_rows(v, v_sn, v_sh, L, H_kv, d_h)) != MOGA_OK)
+  if ((st = check_cross_rows(q, &q_sn, &q_sh, N, H, d_h)) != MOGA_OK ||
+      (st = check_cross_rows(k, &k_sn, &k_sh, L, H_kv, d_h)) != MOGA_OK ||
+      (st = check_cross_rows(v, &v_sn, &v_sh, L, H_kv, d_h)) != MOGA_OK)
     return st;
   a->q = q, a->q_sn = q_sn, a->q_sh = q_sh;
   a->k = k, a->k_sn = k_sn, a->k_sh = k_sh;
@@ -676,6 +681,20 @@ bool make_tmap_box5(CUtensorMap* map, const void* base, uint64_t d_h, uint64_t H
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t d_h, uint64_t H, uint64_t N, uint64_t stride_h,
+                     uint64_t stride_n, uint32_t r, uint32_t tokens) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {d_h, H, N};
+  cuuint64_t strides[2] = {stride_h * 2, stride_n * 2};
+  cuuint32_t box[3] = {64, r, tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult res = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS;
 }
 
 bool make_tmap_tokens(CUtensorMap* map, const void* base, uint64_t d_h, uint64_t H, uint64_t N) {
@@ -1272,6 +1291,7 @@ moga_status moga_cross_attn(const void* q, int64_t q_sn, int64_t q_sh, const voi
   if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
   a.out = out;
   a.lse = lse;
+  a.withhold = g_debug_inject.load(std::memory_order_relaxed) == 1;
   int launches = 0;
   const cudaError_t e = launch_cross_attn(c, a, (uint8_t*)ws + kHeader, &launches);
   count((uint64_t)launches);

@@ -9,10 +9,33 @@
 //   dV = P^T dO,  dK = dS^T Q / sqrt(d_h),  dQ = dS K / sqrt(d_h),
 // with P = exp(S - lse), and dK, dV summed over the query heads that share a
 // key head.
+//
+// cross_fwd_kernel<DH>  persistent, one CTA of 16 warps per SM.  A unit is two
+//   128-row query tiles (A, B) of one (segment, key head): with r = H / H_kv
+//   query heads to a key head a tile holds 128 / r tokens of all r heads
+//   (one TMA box of 64 columns x r heads x 128 / r tokens), so that K and V are
+//   read once for all of them.
+//   warp 0  TMA of the K and V tiles (128 keys);  warp 3  TMA of the query tiles
+//   warp 1  tcgen05.mma: PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); the next unit's
+//           first S follows its last PV without a gap
+//   warp 2  zeroes the rows of a V tile between the segment's last key and the
+//           next multiple of 16 (the product runs in steps of 16 keys; a row of
+//           another segment may hold NaN, and 0 * NaN is NaN)
+//   warps 4-7, 8-11  softmax of tile A, B, one row per thread: S is read from
+//           TMEM once, P is written over it in bf16 and is the A operand of PV
+//   warps 12-15  epilogue of both tiles: O / l from TMEM through 4 KB of shared
+//           memory per warp to 128-byte row pieces.  Prompts are short: with 512
+//           keys a unit has four steps, and an epilogue inside the softmax warps
+//           would take as long as two of them.
+// With few units the key range is split over CTAs, which write O / l and lse in
+// fp32, and cross_join_kernel joins them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moga {
 namespace {
@@ -34,6 +57,7 @@ __device__ __forceinline__ Seg segment(const CrossArgs& a, int s) {
 // length must fit its segment.  Every thread of the block gets the answer.
 __device__ bool segments_ok(const CrossArgs& a, int* status) {
   bool bad = false;
+#pragma unroll 1
   for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
     const Seg g = segment(a, s);
     bad |= g.q0 < 0 || g.q1 < g.q0 || g.q1 > a.N || g.k0 < 0 || g.k1 < g.k0 || g.k1 > a.L;
@@ -159,6 +183,862 @@ __global__ void __launch_bounds__(256) cross_keys_kernel(const CrossArgs a, int*
   }
 }
 
+// ------------------------------------------------------------------ forward on the tensor cores
+constexpr int kXThreads = 512;
+constexpr int kMaxSeg = 1024;
+constexpr int kSplitSms = 148;  // a B200's SMs
+
+constexpr int kFeedSlots = 4;
+constexpr int kFeedReaders = 15;  // K/V, products, rows past the last key: a thread each; softmax and epilogue: 12 warps
+
+template <int DH>
+struct XPlan {
+  static constexpr int kChunks = DH / 64;
+  static constexpr int kStages = DH == 64 ? 4 : 2;
+  static constexpr int kChunk = kTile * 128;         // bytes of 64 columns of a tile
+  static constexpr int kTileBytes = kTile * DH * 2;
+  static constexpr int kQ = 0;                       // tiles A, B
+  static constexpr int kK = 2 * kTileBytes;
+  static constexpr int kV = kK + kStages * kTileBytes;
+  static constexpr int kStage = kV + kStages * kTileBytes;  // epilogue: 4 KB per warp
+  static constexpr int kStat = kStage + 4 * 4096;    // [2 parities][2 tiles][128] of (1 / l, lse)
+  static constexpr int kBar = kStat + 2 * 2 * kTile * 8;
+  static constexpr int kFeed = kBar + 512;           // ring of units
+  static constexpr int kPre = kFeed + kFeedSlots * 32;  // units before each segment
+  static constexpr int kBytes = kPre + (kMaxSeg + 1) * 4 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+struct XUnit {
+  int g;               // key head, or query head without packing
+  int q0, q1;          // this unit's first token, its segment's end
+  int k0, k1;          // keys of this unit (its share of the segment's)
+  int split;
+};
+
+struct XGrid {
+  int tokens;          // tokens of a tile: 128 / r
+  int r, log2r;        // query heads of a tile
+  int splits;
+  int step_w, step_g;  // a step of gridDim.x units, in places and shares, and in heads
+};
+
+// The bounded wait of ptx.cuh without its record of where it gave up: that
+// one, inlined at some twenty places, made the kernel 114 KB of instructions,
+// and what a role runs once a unit was fetched anew each time (a unit's end
+// took the softmax 3,900 cycles).
+template <int kSleep = 0>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
+  uint32_t n = 0, t0 = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    if (kSleep > 0) __nanosleep(kSleep);
+    if (++n & 63u) continue;
+    const uint32_t t = (uint32_t)(global_timer_ns() >> 10);  // about a microsecond
+    if (n == 64) t0 = t;
+    if (t - t0 > (uint32_t)(c.limit_ns >> 10)) {
+      *c.abort_flag = 1;
+      if (c.status) atomicOr(c.status, DEV_TIMEOUT);
+    }
+    if (*c.abort_flag) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+
+// The products with descriptors of 128-byte swizzled operands (8-row groups
+// 1,024 bytes apart) given by their low words: the high word is a constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
+      : "memory");
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// mbar_try_wait without its suspension.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ int steps_of(const XUnit& u) { return (u.k1 - u.k0 + kTile - 1) / kTile; }
+
+// A CTA's units are blockIdx.x, then every gridDim.x-th, the heads of a place
+// next to one another (CTAs that run at once read whole token rows).  One
+// thread walks them, carrying head, place and segment along, and hands each
+// to the other roles through a ring in shared memory: with the walk in every
+// role the code that runs did not fit the instruction cache.
+struct Feed {
+  int4* ring;          // [kFeedSlots][2]: (g, q0, q1, split), (k0, k1, 1 or 0 at the end, -)
+  uint64_t* full;
+  uint64_t* empty;
+  uint32_t n;
+  // The next unit; false: none is left, or a wait gave up.  `warp`: all of a
+  // warp's threads read, and its first one frees the slot.
+  template <bool kWarp, int kSleep = 0>
+  __device__ __forceinline__ bool next(XUnit& u, const WaitCtx& wc) {
+    const uint32_t s = n % kFeedSlots;
+    if (!wait_for<kSleep>(&full[s], (n / kFeedSlots) & 1, wc)) return false;
+    const int4 a = ring[2 * s], b = ring[2 * s + 1];
+    if (kWarp) __syncwarp();
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
+    ++n;
+    u = XUnit{a.x, a.y, a.z, b.x, b.y, a.w};
+    return b.z != 0;
+  }
+  __device__ __forceinline__ bool put(const XUnit& u, int more, const WaitCtx& wc) {
+    const uint32_t s = n % kFeedSlots;
+    if (!wait_for(&empty[s], ((n / kFeedSlots) & 1) ^ 1, wc)) return false;
+    ring[2 * s] = make_int4(u.g, u.q0, u.q1, u.split);
+    ring[2 * s + 1] = make_int4(u.k0, u.k1, more, 0);
+    mbar_arrive(&full[s]);
+    ++n;
+    return true;
+  }
+};
+
+struct Walk {
+  const CrossArgs& a;
+  const XGrid& x;
+  const int* pre;
+  int heads;           // units of a place: one per key head, or per query head without packing
+  int left;            // units to come
+  int g, w, s;         // head; place and share; segment
+  Seg seg;
+  __device__ __forceinline__ Walk(const CrossArgs& a_, const XGrid& x_, const int* pre_) : a(a_), x(x_), pre(pre_) {
+    heads = a.H >> x.log2r;
+    const int total = pre[a.S] * x.splits * heads;
+    left = (int)blockIdx.x < total ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+    w = (int)blockIdx.x / heads;
+    g = (int)blockIdx.x - w * heads;
+    s = 0;
+    seg = segment(a, 0);
+  }
+  __device__ __forceinline__ bool next(XUnit& u) {
+    if (left-- <= 0) return false;
+    int p = w;
+    u.split = 0;
+    if (x.splits > 1) {
+      p = (int)((unsigned)w / (unsigned)x.splits);
+      u.split = w - p * x.splits;
+    }
+    if (p >= pre[s + 1]) {  // some segments have no place
+#pragma unroll 1
+      do ++s; while (p >= pre[s + 1]);
+      seg = segment(a, s);
+    }
+    u.g = g;
+    u.q0 = seg.q0 + (p - pre[s]) * 2 * x.tokens;
+    u.q1 = seg.q1;
+    u.k0 = seg.k0;
+    u.k1 = seg.k1;
+    if (x.splits > 1) {
+      const unsigned n = (unsigned)(seg.k1 - seg.k0 + kTile - 1) / kTile, each = n / (unsigned)x.splits,
+                     over = n - each * (unsigned)x.splits;  // the first `over` shares have one tile more
+      const unsigned t0 = each * (unsigned)u.split + min((unsigned)u.split, over);
+      u.k0 = seg.k0 + (int)(t0 * kTile);
+      u.k1 = min(seg.k1, u.k0 + (int)((each + ((unsigned)u.split < over ? 1u : 0u)) * kTile));
+    }
+    w += x.step_w;
+    g += x.step_g;
+    if (g >= heads) {
+      g -= heads;
+      ++w;
+    }
+    return true;
+  }
+};
+
+// pre[s] = places (pairs of query tiles) before segment s.
+__device__ void place_table(const CrossArgs& a, int per_place, int* pre) {
+  int run = 0;
+#pragma unroll 1
+  for (int base = 0; base < a.S; base += 32) {  // warp 0 alone: S / 32 rounds
+    if (threadIdx.x < 32) {
+      const int s = base + (int)threadIdx.x;
+      int n = 0;
+      if (s < a.S) {
+        const Seg g = segment(a, s);
+        n = (g.q1 - g.q0 + per_place - 1) / per_place;
+      }
+      int sum = n;
+#pragma unroll
+      for (int m = 1; m < 32; m <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, sum, m);
+        if ((int)threadIdx.x >= m) sum += t;
+      }
+      if (s < a.S) pre[s] = run + sum - n;
+      run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  if (threadIdx.x == 0) pre[a.S] = run;
+}
+
+// Head h's rows in a 2-D view of a [n, heads, d_h] tensor: column h * x + c,
+// row h * y + token (token-major: y = 0; head-major: x = 0).
+struct XView {
+  int x, y;
+};
+
+struct XMaps {
+  CUtensorMap q, k, v;
+  XView qv, kv, vv;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(kXThreads, 1)
+cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid xg, float* part_o, float* part_lse,
+                 int withhold, int* status, unsigned long long wait_ns) {
+  using P = XPlan<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
+  uint64_t* q_full = bars;                     // [2]
+  uint64_t* q_empty = bars + 2;                // [2]
+  uint64_t* s_full = bars + 4;                 // [2]: S of tile A / B computed
+  uint64_t* p_full = bars + 6;                 // [2]: P written (O rescaled)
+  uint64_t* o_full = bars + 8;                 // [2]: a unit's last P V done
+  uint64_t* o_empty = bars + 10;               // [2]: O read by the epilogue
+  uint64_t* stat_full = bars + 12;             // [2 parities][2 tiles]: a unit's row sums written
+  uint64_t* k_full = bars + 16;                // [kStages] each
+  uint64_t* k_empty = k_full + P::kStages;
+  uint64_t* v_full = k_empty + P::kStages;
+  uint64_t* v_ready = v_full + P::kStages;     // rows past the last key zeroed
+  uint64_t* v_empty = v_ready + P::kStages;
+  uint64_t* f_full = v_empty + P::kStages;      // [kFeedSlots] each: the ring of units
+  uint64_t* f_empty = f_full + kFeedSlots;
+  uint64_t* done_bar = f_empty + kFeedSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(done_bar + 2);
+  static_assert(16 + 5 * P::kStages + 2 * kFeedSlots + 3 <= 64, "barrier area holds 64 words");
+  int* pre = reinterpret_cast<int*>(smem + P::kPre);
+  float2* stat = reinterpret_cast<float2*>(smem + P::kStat);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (!segments_ok(a, status)) return;
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 128);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&o_empty[x], 128);
+      mbar_init(&stat_full[x], 128);
+      mbar_init(&stat_full[2 + x], 128);
+    }
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_ready[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < kFeedSlots; ++s) {
+      mbar_init(&f_full[s], 1);
+      mbar_init(&f_empty[s], kFeedReaders);
+    }
+    mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  place_table(a, 2 * xg.tokens, pre);
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM: S and P of tile A [0, 128), of tile B [128, 256), O of A [256, ..), O of B [384, ..)
+  auto tS = [tmem](int x) { return tmem + (uint32_t)(x * 128); };
+  auto tO = [tmem](int x) { return tmem + 256u + (uint32_t)(x * 128); };
+  WaitCtx wc{abort_flag, status, wait_ns};
+  const int share = a.H / a.Hkv;
+  Feed feed{reinterpret_cast<int4*>(smem + P::kFeed), f_full, f_empty, 0};
+  XUnit u{};
+
+  if (warp < 4) {
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- K and V tiles
+      tma_prefetch_desc(&m.k);
+      tma_prefetch_desc(&m.v);
+      const uint64_t keep = l2_policy_evict_last();
+      uint32_t t = 0;
+      bool ok = true, kv_pending = false;  // kv_pending: the last K has no V behind it
+      while (ok && feed.next<false>(u, wc)) {
+        const int n = steps_of(u);
+        const int hk = xg.r > 1 ? u.g : u.g / share;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+          const int s = (int)(t % P::kStages);
+          const uint32_t ph = ((t / P::kStages) & 1) ^ 1;
+          const int row = u.k0 + j * kTile;
+          if (!wait_for(&k_empty[s], ph, wc)) { ok = false; break; }
+          if (withhold && t == 0) { ok = false; break; }  // test hook: this tile never comes
+          mbar_expect_tx(&k_full[s], P::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < P::kChunks; ++c)
+            tma_load_2d_hint(&m.k, &k_full[s], smem + P::kK + s * P::kTileBytes + c * P::kChunk, hk * m.kv.x + c * 64,
+                             hk * m.kv.y + row, keep);
+          kv_pending = true;
+          if (!wait_for(&v_empty[s], ph, wc)) { ok = false; break; }
+          mbar_expect_tx(&v_full[s], P::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < P::kChunks; ++c)
+            tma_load_2d_hint(&m.v, &v_full[s], smem + P::kV + s * P::kTileBytes + c * P::kChunk, hk * m.vv.x + c * 64,
+                             hk * m.vv.y + row, keep);
+          kv_pending = false;
+          ++t;
+        }
+      }
+      // Every load has landed before the CTA exits.
+      volatile int zero = 0;
+      WaitCtx dc{&zero, nullptr, 100000000ull};
+      const uint32_t tk = t + (kv_pending ? 1 : 0);
+      for (uint32_t s = 0; s < (uint32_t)P::kStages; ++s) {
+        if (s < tk) wait_for(&k_full[s], ((tk - 1 - s) / P::kStages) & 1, dc);
+        if (s < t) wait_for(&v_full[s], ((t - 1 - s) / P::kStages) & 1, dc);
+      }
+    } else if (warp == 3 && lane == 0) {
+      // -------------------------------------------------------------- units, and their query tiles
+      tma_prefetch_desc(&m.q);
+      const uint64_t once = l2_policy_evict_first();
+      uint32_t n[2] = {0, 0};
+      bool ok = true;
+      Walk it(a, xg, pre);
+      while (ok) {
+        const bool more = it.next(u);
+        if (!feed.put(u, more ? 1 : 0, wc) || !more) break;
+        if (steps_of(u) == 0) continue;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int tok = u.q0 + x * xg.tokens;
+          if (tok >= u.q1) break;
+          if (!wait_for(&q_empty[x], (n[x] & 1) ^ 1, wc)) { ok = false; break; }
+          mbar_expect_tx(&q_full[x], P::kTileBytes);
+#pragma unroll
+          for (int c = 0; c < P::kChunks; ++c) {
+            uint8_t* dst = smem + P::kQ + x * P::kTileBytes + c * P::kChunk;
+            if (xg.r > 1)
+              tma_load_3d(&m.q, &q_full[x], dst, c * 64, u.g * xg.r, tok);
+            else
+              tma_load_2d_hint(&m.q, &q_full[x], dst, u.g * m.qv.x + c * 64, u.g * m.qv.y + tok, once);
+          }
+          ++n[x];
+        }
+      }
+      volatile int zero = 0;
+      WaitCtx dc{&zero, nullptr, 100000000ull};
+      for (int x = 0; x < 2; ++x)
+        if (n[x] > 0) wait_for(&q_full[x], (n[x] - 1) & 1, dc);
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- rows past the last key
+      uint32_t t = 0;
+      bool ok = true;
+      // Lane 0 reads the units and waits for the tiles.
+      while (ok) {
+        int w = 1;
+        if (lane == 0) w = feed.next<false>(u, wc);
+        if (!__shfl_sync(0xffffffffu, w, 0)) break;
+        const int keys = __shfl_sync(0xffffffffu, u.k1 - u.k0, 0), n = (keys + kTile - 1) / kTile;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++t) {
+          const int s = (int)(t % P::kStages);
+          w = 1;
+          if (lane == 0) w = wait_for(&v_full[s], (t / P::kStages) & 1, wc);
+          if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+          __syncwarp();
+          const int valid = keys - j * kTile;
+          if (valid < kTile) {
+            const int end = min((valid + 15) & ~15, kTile);
+            uint8_t* v = smem + P::kV + s * P::kTileBytes;
+#pragma unroll 1
+            for (int i = lane; i < (end - valid) * 8 * P::kChunks; i += 32) {
+              const int piece = i & 7, c = (i >> 3) % P::kChunks, r = valid + (i >> 3) / P::kChunks;
+              *reinterpret_cast<uint4*>(v + c * P::kChunk + r * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(&v_ready[s]);
+        }
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- products
+      // The whole warp walks the steps, one elected lane issues.
+      const bool leader = elect_one();
+      // One place in the code for S and one for P V, with the tile (0: A, 1: B)
+      // as a value, and 32-bit descriptor arithmetic: the role stays small.
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idO = idesc_bf16(128, DH, false, true);
+      const uint32_t q_lo = desc_lo(smem_u32(smem + P::kQ), 16), k_lo = desc_lo(smem_u32(smem + P::kK), 16),
+                     v_lo = desc_lo(smem_u32(smem + P::kV), P::kChunk);
+      uint32_t kt = 0, vt = 0;             // key and value tiles taken
+      uint32_t qph = 0, pph = 0, oph = 0;  // phases of q_full, p_full, o_empty: bit x
+      uint32_t used = 0;                   // bit x: tile x has had a unit
+      XUnit nu{};                          // the next unit with keys
+      bool left = true;                    // units may be left
+      int n = 0, j = 0;
+      bool have = false;                   // before the first unit there is no step, only the next S
+      while (true) {
+        const bool more = have && j + 1 < n;
+        bool next = more;                  // is there an S to issue
+        if (!more)
+          while (left && !next) {
+            left = feed.next<true>(nu, wc);
+            next = left && nu.k1 > nu.k0;
+          }
+        if (!have && !next) break;
+        const int valid = u.k1 - u.k0 - j * kTile;
+        const int nvalid = more ? valid - kTile : nu.k1 - nu.k0;
+        const bool nb = more ? u.q0 + xg.tokens < u.q1 : nu.q0 + xg.tokens < nu.q1;
+        const int vs = (int)(vt % P::kStages), ks = (int)(kt % P::kStages);
+        const uint32_t kph = (kt / P::kStages) & 1;
+        if (have && !wait_for(&v_ready[vs], (vt / P::kStages) & 1, wc)) break;
+        if (more && !wait_for(&k_full[ks], kph, wc)) break;
+        int y = 0;                         // the next S to issue
+        bool ok = true;
+#pragma unroll 1
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (have && (x == 0 || u.q0 + xg.tokens < u.q1)) {
+            // O_x += P_x V in steps of 16 keys, once P is written and O_x free of the unit before
+            ok = wait_for(&p_full[x], (pph >> x) & 1, wc);
+            pph ^= 1u << x;
+            if (j == 0) {
+              if (ok && ((used >> x) & 1)) {
+                ok = wait_for(&o_empty[x], (oph >> x) & 1, wc);
+                oph ^= 1u << x;
+              }
+              used |= 1u << x;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t vd = v_lo + (uint32_t)(vs * (P::kTileBytes >> 4));
+            uint32_t ts = tS(x);
+            const uint32_t to = tO(x);
+            if (!leader) {
+            } else if (valid >= kTile) {
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk) umma_ts_lo(to, ts + kk * 8, vd + kk * 128, idO, (uint32_t)(j + kk));
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk * 16 < valid; ++kk, ts += 8, vd += 128) umma_ts_lo(to, ts, vd, idO, (uint32_t)(j + kk));
+            }
+            if (!more && leader) umma_commit(&o_full[x]);
+          }
+          if (!next) continue;
+          // At a unit's end S_A of the next one goes before this one's PV_B if its operands are here.
+          if (x == 0 && !more && have && !(mbar_test(&k_full[ks], kph) && mbar_test(&q_full[0], qph & 1))) continue;
+#pragma unroll 1
+          for (; y <= x && ok; ++y) {
+            if (y == 1 && !nb) break;
+            if (!more) {
+              ok = (y == 1 || wait_for(&k_full[ks], kph, wc)) && wait_for(&q_full[y], (qph >> y) & 1, wc);
+              qph ^= 1u << y;
+              if (!ok) break;
+            }
+            tc_fence_after();
+            // S_y = Q_y K^T over all 128 rows of the key tile: what lies past the last key is masked
+            const uint32_t qd = q_lo + (uint32_t)(y * (P::kTileBytes >> 4)), kd = k_lo + (uint32_t)(ks * (P::kTileBytes >> 4));
+            const uint32_t ts = tS(y);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * P::kChunk + (kk & 3) * 32) >> 4;
+                umma_lo(ts, qd + o, kd + o, idS, (uint32_t)kk);
+              }
+              umma_commit(&s_full[y]);
+              if (nvalid <= kTile) umma_commit(&q_empty[y]);  // the unit's last S
+            }
+          }
+        }
+        if (!ok) break;
+        if (have) {
+          if (leader) umma_commit(&v_empty[vs]);
+          ++vt;
+        }
+        if (next) {
+          if (leader) umma_commit(&k_empty[ks]);
+          ++kt;
+        }
+        if (more) {
+          ++j;
+        } else {
+          u = nu;
+          n = steps_of(u);
+          j = 0;
+          have = next;
+        }
+      }
+      if (leader) umma_commit(done_bar);
+      volatile int zero = 0;
+      WaitCtx dc{&zero, nullptr, 100000000ull};
+      wait_for(done_bar, 0, dc);
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2, sub = warp & 3, row = sub * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
+    const uint32_t tSx = tS(x) + lane_base, tOx = tO(x) + lane_base;
+    const float scale_log2 = 1.4426950408889634f * rsqrtf((float)DH);
+    uint32_t sc = 0, un = 0;
+    bool ok = true;
+    while (ok && feed.next<true>(u, wc)) {
+      const int n = steps_of(u);
+      if (n == 0 || u.q0 + x * xg.tokens >= u.q1) continue;
+      float m_run = -INFINITY;
+      uint64_t l2 = f2_pack(0.f, 0.f);
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if (!wait_for(&s_full[x], sc & 1, wc)) { ok = false; break; }
+        ++sc;
+        tc_fence_after();
+        const int valid = u.k1 - u.k0 - j * kTile;
+        if (valid < kTile) {
+          // Columns past the last key: -inf, written to TMEM (as selects on
+          // the registers they were a sixth of the kernel's instructions).
+          const float inf = -INFINITY;
+          int c = valid;
+#pragma unroll 1
+          for (; c & 15; ++c) tmem_st1(tSx + c, inf);
+#pragma unroll 1
+          for (; c < kTile; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = inf;
+            tmem_st16u(tSx + c, reinterpret_cast<const uint32_t*>(v));
+          }
+          tmem_st_wait();
+        }
+        // Half of the row at a time in registers, the first half last so that
+        // it need not be read again: the exponentials below are then one loop
+        // body of 64 columns.  Unrolled over all 128 the kernel's running code
+        // did not fit the instruction cache (12 % of fetches missed).
+        float sr[64];
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int half = 1; half >= 0; --half) {
+          tmem_ld32(tSx + half * 64, sr);
+          tmem_ld32(tSx + half * 64 + 32, sr + 32);
+          tmem_ld_wait();
+          float m4[4];  // four chains of three-input maxima
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            m4[i] = fmax3(sr[16 * i], sr[16 * i + 1], sr[16 * i + 2]);
+#pragma unroll
+            for (int k = 3; k + 1 < 16; k += 2) m4[i] = fmax3(m4[i], sr[16 * i + k], sr[16 * i + k + 1]);
+            m4[i] = fmaxf(m4[i], sr[16 * i + 15]);
+          }
+          mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        const float m_new = fmaxf(m_run, mx * scale_log2);
+        // The maximum moves, and O is rescaled, only when it grows by more
+        // than 2^8; P and l share the older one otherwise.
+        float alpha = 1.0f;
+        bool rescale = false;
+        if (j == 0) {
+          m_run = m_new;
+        } else {
+          const bool need = m_new > m_run + 8.0f;
+          rescale = __any_sync(0xffffffffu, need);
+          if (need) {
+            alpha = fast_exp2(m_run - m_new);
+            l2 = f2_mul(l2, f2_pack(alpha, alpha));
+            m_run = m_new;
+          }
+        }
+        // P = 2^(S scale - m) to bf16, the operand's type: rounding it by 2^-9
+        // of itself keeps O within what its own bf16 holds.  l sums it unrounded.
+        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_run, -m_run);
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int half = 0; half * 64 < min(valid, kTile); ++half) {  // P V stops at the last key's 16
+          if (half) {
+            tmem_ld32(tSx + 64, sr);
+            tmem_ld32(tSx + 96, sr + 32);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float t0, t1;
+              f2_unpack(f2_fma(f2_pack(sr[c * 32 + 2 * e], sr[c * 32 + 2 * e + 1]), sc2, nm2), t0, t1);
+              t0 = fast_exp2(t0);
+              t1 = fast_exp2(t1);
+              acc[e & 3] = f2_add(acc[e & 3], f2_pack(t0, t1));
+              pk[e] = pack_bf16x2(t0, t1);
+            }
+            tmem_st16u(tSx + half * 32 + c * 16, pk);
+          }
+        }
+        l2 = f2_add(l2, f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])));
+        if (rescale) {
+#pragma unroll 1
+          for (int c = 0; c < DH; c += 16) {
+            float o[16];
+            tmem_ld16(tOx + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= alpha;
+            tmem_st16u(tOx + c, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[x]);
+      }
+      if (!ok) break;
+      float l0, l1;
+      f2_unpack(l2, l0, l1);
+      const float l = l0 + l1;
+      // The slot of unit un + 2 is written only after the epilogue of unit un
+      // has freed O, which P V of unit un + 1 waited for.
+      stat[(un & 1) * 2 * kTile + x * kTile + row] = make_float2(1.0f / l, (m_run + log2f(l)) * 0.6931471805599453f);
+      mbar_arrive(&stat_full[(un & 1) * 2 + x]);
+      ++un;
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int sub = warp & 3, row = sub * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
+    uint8_t* stage = smem + P::kStage + sub * 4096;
+    uint32_t un0 = 0, un1 = 0;  // units of tile A, B
+    bool ok = true;
+    while (ok && feed.next<true, 100>(u, wc)) {
+      const bool keys = steps_of(u) > 0;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const int tok0 = u.q0 + x * xg.tokens;
+        if (tok0 >= u.q1) break;
+        float2 st = make_float2(0.0f, -INFINITY);
+        if (keys) {
+          const uint32_t n = x ? un1++ : un0++;
+          if (!wait_for<100>(&stat_full[(n & 1) * 2 + x], (n >> 1) & 1, wc) ||
+              !wait_for<20>(&o_full[x], n & 1, wc)) { ok = false; break; }
+          tc_fence_after();
+          st = stat[(n & 1) * 2 * kTile + x * kTile + row];
+        }
+        // This thread's row: token and query head.
+        auto place = [&](int r, int& tok, int& h) {
+          tok = tok0 + (r >> xg.log2r);
+          h = (u.g << xg.log2r) + (r & (xg.r - 1));
+          return tok < u.q1;
+        };
+        int tok, h;
+        const bool live = place(row, tok, h);
+        float* lse = part_lse ? part_lse + (int64_t)u.split * a.H * a.N : a.lse;
+        if (lse && live) lse[(int64_t)h * a.N + tok] = st.y;
+        if (part_o && !keys) continue;  // the join leaves a share without keys out
+        const uint32_t to = tO(x) + lane_base;
+        const int piece = lane & 7, sub8 = lane >> 3;
+        uint8_t* mine = stage + lane * 128;
+        // 128 bytes of each of the warp's rows go through shared memory at a
+        // time: written by row, read back as whole 128-byte pieces, four rows
+        // to a store.
+        auto store_rows = [&](uint8_t* base, int row_bytes) {
+          __syncwarp();
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + sub8;
+            v[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + ((piece ^ (r & 7)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            int t, hh;
+            if (place(sub * 32 + i * 4 + sub8, t, hh))
+              __stcs(reinterpret_cast<uint4*>(base + (int64_t)(t * a.H + hh) * row_bytes + piece * 16), v[i]);
+          }
+          __syncwarp();
+        };
+        if (!part_o) {
+          uint32_t w[DH / 2];  // the row in bf16
+#pragma unroll
+          for (int c = 0; c < DH / 32; ++c) {
+            float o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[c * 16 + e] = keys ? pack_bf16x2(o[2 * e] * st.x, o[2 * e + 1] * st.x) : 0;
+          }
+          if (keys) {  // all of O is read
+            tc_fence_before();
+            mbar_arrive(&o_empty[x]);
+          }
+#pragma unroll
+          for (int c = 0; c < DH / 64; ++c) {
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              *reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)) =
+                  make_uint4(w[c * 32 + p * 4], w[c * 32 + p * 4 + 1], w[c * 32 + p * 4 + 2], w[c * 32 + p * 4 + 3]);
+            store_rows(static_cast<uint8_t*>(a.out) + c * 128, DH * 2);
+          }
+        } else {  // a share of the keys: O / l in fp32
+          uint8_t* base = reinterpret_cast<uint8_t*>(part_o + (int64_t)u.split * a.N * a.H * DH);
+#pragma unroll 1
+          for (int c = 0; c < DH / 32; ++c) {
+            float o[32];
+            tmem_ld32(to + c * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              *reinterpret_cast<float4*>(mine + ((p ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * p] * st.x, o[4 * p + 1] * st.x, o[4 * p + 2] * st.x, o[4 * p + 3] * st.x);
+            if (c + 1 == DH / 32) {
+              tc_fence_before();
+              mbar_arrive(&o_empty[x]);
+            }
+            store_rows(base + c * 128, DH * 4);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// out and lse from the splits' O / l and lse: out = sum_s exp(lse_s - lse) O_s.
+// One warp per (token, head) of a segment; a share without keys has lse = -inf.
+template <int DH>
+__global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int splits, const float* __restrict__ part_o,
+                                                         const float* __restrict__ part_lse, int* status) {
+  constexpr int C = DH / 32;
+  if (!segments_ok(a, nullptr)) return;  // the kernel before reported it
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (w >= a.N * a.H) return;
+  const int64_t n = w / a.H;
+  const int h = (int)(w - n * a.H);
+  bool inside = a.q_off == nullptr;
+  if (!inside) inside = n >= a.q_off[0] && n < a.q_off[a.S];  // segments follow one another
+  if (!inside) return;
+  const int64_t rows = a.N * a.H, at = (int64_t)h * a.N + n;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lse[s * rows + at]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  float l = 0.0f, o[C] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float e = part_lse[s * rows + at];
+    if (e == -INFINITY) continue;
+    const float f = expf(e - m);
+    l += f;
+    const float* p = part_o + (s * rows + w) * DH + lane * C;
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = fmaf(f, p[i], o[i]);
+  }
+  store_row<C>(a.out, w * DH, lane, o, l > 0.0f ? 1.0f / l : 0.0f);
+  if (a.lse && lane == 0) a.lse[at] = m + logf(l);
+}
+
+// 2-D view of a [n, heads, d_h] tensor whose box is 64 columns x 128 tokens of a head.
+bool view_2d(CUtensorMap* map, XView* v, const void* base, int64_t sn, int64_t sh, int64_t n, int H, int d_h) {
+  if (n == 0) return true;  // nothing is read through it
+  if (H == 1 || sn >= (H - 1) * sh + d_h) {  // token-major
+    *v = XView{(int)sh, 0};
+    return make_tmap_2d(map, base, (uint64_t)((H - 1) * sh + d_h), (uint64_t)n, (uint64_t)sn * 2, kTile);
+  }
+  *v = XView{0, (int)(sh / sn)};
+  return make_tmap_2d(map, base, (uint64_t)d_h, (uint64_t)(H - 1) * (sh / sn) + n, (uint64_t)sn * 2, kTile);
+}
+
+// Query heads of a tile: all that share a key head, where they are a power of
+// two up to 64 and q is token-major with a token stride in whole head strides.
+int pack_of(const CrossArgs& a) {
+  const int r = a.H / a.Hkv;
+  if (r < 2 || r > 64 || (r & (r - 1))) return 1;
+  return a.q_sn >= (a.H - 1) * a.q_sh + a.d_h && a.q_sn % a.q_sh == 0 ? r : 1;
+}
+
+// Places (pairs of query tiles) of a call, at most: each segment may add a ragged one.
+int64_t places_most(int64_t N, int r, int S) { return N == 0 ? 0 : ceil_div(N, 2 * kTile / r) + std::min<int64_t>(S, N) - 1; }
+
+// Shares of the keys: enough units for every SM, each of two key tiles at least.
+int splits_of(int64_t N, int64_t L, int H, int r, int S) {
+  const int64_t units = places_most(N, r, S) * (H / r);
+  if (units == 0 || units >= kSplitSms) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kSplitSms / units, ceil_div(ceil_div(L, S), 2 * kTile)));
+}
+
+template <int DH>
+cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches) {
+  using P = XPlan<DH>;
+  XMaps m{};
+  XGrid x;
+  x.r = pack_of(a);
+  x.log2r = 0;
+  while (1 << x.log2r < x.r) ++x.log2r;
+  x.tokens = kTile / x.r;
+  x.splits = splits_of(a.N, a.L, a.H, x.r, a.S);
+  bool ok = view_2d(&m.k, &m.kv, a.k, a.k_sn, a.k_sh, a.L, a.Hkv, DH) &&
+            view_2d(&m.v, &m.vv, a.v, a.v_sn, a.v_sh, a.L, a.Hkv, DH);
+  ok = ok && (x.r > 1 ? make_tmap_heads(&m.q, a.q, DH, a.H, a.N, a.q_sh, a.q_sn, x.r, x.tokens)
+                      : view_2d(&m.q, &m.qv, a.q, a.q_sn, a.q_sh, a.N, a.H, DH));
+  if (!ok) return cudaErrorInvalidValue;
+  float *po = nullptr, *pl = nullptr;
+  if (x.splits > 1) {
+    pl = reinterpret_cast<float*>(ws);
+    po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 4, 256));
+  }
+  cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t units = places_most(a.N, x.r, a.S) * x.splits * (a.H / x.r);
+  const unsigned grid = (unsigned)std::min<int64_t>(units, c.num_sms);
+  x.step_w = (int)grid / (a.H / x.r);
+  x.step_g = (int)grid % (a.H / x.r);
+  cross_fwd_kernel<DH><<<grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, po, pl, a.withhold, c.status,
+                                                                 (unsigned long long)c.wait_ns);
+  *launches = 1;
+  if ((e = cudaGetLastError()) != cudaSuccess || x.splits == 1) return e;
+  cross_join_kernel<DH><<<(unsigned)ceil_div(a.N * a.H, 8), 256, 0, c.stream>>>(a, x.splits, po, pl, c.status);
+  *launches = 2;
+  return cudaGetLastError();
+}
+
 unsigned blocks_for(const DevCtx& c, int64_t warps) {
   const int64_t b = ceil_div(warps, 8), cap = (int64_t)c.num_sms * 64;
   return (unsigned)(b < cap ? b : cap);
@@ -166,15 +1046,22 @@ unsigned blocks_for(const DevCtx& c, int64_t warps) {
 
 }  // namespace
 
-size_t cross_fwd_ws_bytes(int64_t, int64_t, int, int, int, int) { return 0; }
+size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S) {
+  // Packed or not is known with the strides only: the larger of the two.
+  size_t most = 0;
+  for (int r : {1, H / H_kv}) {
+    if (r < 1 || r > 64 || (r & (r - 1))) continue;
+    const int64_t splits = splits_of(N, L, H, r, S);
+    if (splits > 1) most = std::max(most, align_up((size_t)(splits * N * H * 4), 256) + (size_t)(splits * N * H * d_h * 4));
+  }
+  return most;
+}
 size_t cross_bwd_ws_bytes(int64_t N, int64_t, int H, int, int, int) { return (size_t)N * H * 4; }
 
-cudaError_t launch_cross_attn(const DevCtx& c, const CrossArgs& a, uint8_t*, int* launches) {
+cudaError_t launch_cross_attn(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches) {
   *launches = 0;
   if (a.N == 0) return cudaSuccess;
-  (a.d_h == 128 ? cross_rows_kernel<128, false> : cross_rows_kernel<64, false>)<<<blocks_for(c, a.N * a.H), 256, 0, c.stream>>>(a, c.status);
-  *launches = 1;
-  return cudaGetLastError();
+  return a.d_h == 128 ? launch_fwd<128>(c, a, ws, launches) : launch_fwd<64>(c, a, ws, launches);
 }
 
 cudaError_t launch_cross_bwd(const DevCtx& c, const CrossArgs& args, uint8_t* ws, int* launches) {

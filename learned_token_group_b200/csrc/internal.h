@@ -194,6 +194,7 @@ struct CrossArgs {
   void* dk;               // bf16 [L, H_kv, d_h]
   void* dv;
   float* dsum;            // [H, N]
+  int withhold;           // test hook: the forward's first K tile never comes
 };
 size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
 size_t cross_bwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
@@ -240,6 +241,10 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t o
 // with a box of 64 columns x 1 head x 128 tokens and 128-byte swizzle: one
 // box is a 128-row operand tile of one head, read in place.
 bool make_tmap_tokens(CUtensorMap* map, const void* base, uint64_t d_h, uint64_t H, uint64_t N);
+// Encodes a 3-D bf16 tensor map over [N tokens, H heads, d_h] at the given
+// strides (elements) with a box of 64 columns x r heads x tokens.
+bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t d_h, uint64_t H, uint64_t N, uint64_t stride_h,
+                     uint64_t stride_n, uint32_t r, uint32_t tokens);
 // Encodes a 5-D bf16 tensor map over the (d_h, H, Wg, Hg, T) view of a
 // [T*Hg*Wg, H, d_h] tensor with a box of 64 columns x 1 head x window[2] x
 // window[1] x window[0] and 128-byte swizzle: one box is one STGA window of
