@@ -223,14 +223,23 @@ struct XGrid {
   int step_w, step_g;  // a step of gridDim.x units, in places and shares, and in heads
 };
 
-// The bounded wait of ptx.cuh without its record of where it gave up: that
-// one, inlined at some twenty places, made the kernel 114 KB of instructions,
-// and what a role runs once a unit was fetched anew each time (a unit's end
-// took the softmax 3,900 cycles).
-template <int kSleep = 0>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
+// The bounded wait of ptx.cuh, its loop out of line.  What runs here has to
+// fit the instruction cache: with that one inlined at some twenty places the
+// kernel had 114 KB of instructions, and a role's code was fetched anew each
+// time it came round (187,200 x 512 keys: 745 us; 613 us with 45 KB).
+template <int kSleep>
+__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, const WaitCtx c) {
   uint32_t n = 0, t0 = 0;
-  while (!mbar_try_wait(bar, parity)) {
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
     if (kSleep > 0) __nanosleep(kSleep);
     if (++n & 63u) continue;
     const uint32_t t = (uint32_t)(global_timer_ns() >> 10);  // about a microsecond
@@ -241,7 +250,10 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
     }
     if (*c.abort_flag) return false;
   }
-  return true;
+}
+template <int kSleep = 0>
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
+  return mbar_try_wait(bar, parity) || wait_more<kSleep>(smem_u32(bar), parity, c);
 }
 
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
@@ -602,10 +614,11 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       }
     } else if (warp == 1) {
       // -------------------------------------------------------------- products
-      // The whole warp walks the steps, one elected lane issues.
+      // The whole warp walks the steps, one elected lane issues (a single
+      // lane in the role took 12 % longer: nothing in it counts as uniform).
+      // The loop over tiles is unrolled: as values they cost 8 %.
       const bool leader = elect_one();
-      // One place in the code for S and one for P V, with the tile (0: A, 1: B)
-      // as a value, and 32-bit descriptor arithmetic: the role stays small.
+      // 32-bit descriptor arithmetic (the high words are constant) keeps the issue short.
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idO = idesc_bf16(128, DH, false, true);
       const uint32_t q_lo = desc_lo(smem_u32(smem + P::kQ), 16), k_lo = desc_lo(smem_u32(smem + P::kK), 16),
@@ -635,8 +648,9 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         if (more && !wait_for(&k_full[ks], kph, wc)) break;
         int y = 0;                         // the next S to issue
         bool ok = true;
-#pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) break;
           if (have && (x == 0 || u.q0 + xg.tokens < u.q1)) {
             // O_x += P_x V in steps of 16 keys, once P is written and O_x free of the unit before
             ok = wait_for(&p_full[x], (pph >> x) & 1, wc);
@@ -891,25 +905,26 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           __syncwarp();
         };
         if (!part_o) {
-          uint32_t w[DH / 2];  // the row in bf16
-#pragma unroll
-          for (int c = 0; c < DH / 32; ++c) {
-            float o[32];
-            tmem_ld32(to + c * 32, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) w[c * 16 + e] = keys ? pack_bf16x2(o[2 * e] * st.x, o[2 * e + 1] * st.x) : 0;
-          }
-          if (keys) {  // all of O is read
-            tc_fence_before();
-            mbar_arrive(&o_empty[x]);
-          }
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < DH / 64; ++c) {
+            float o[64];
+            tmem_ld32(to + c * 64, o);
+            tmem_ld32(to + c * 64 + 32, o + 32);
+            tmem_ld_wait();
+            if (keys && c + 1 == DH / 64) {  // all of O is read
+              tc_fence_before();
+              mbar_arrive(&o_empty[x]);
+            }
 #pragma unroll
-            for (int p = 0; p < 8; ++p)
-              *reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)) =
-                  make_uint4(w[c * 32 + p * 4], w[c * 32 + p * 4 + 1], w[c * 32 + p * 4 + 2], w[c * 32 + p * 4 + 3]);
+            for (int p = 0; p < 8; ++p) {
+              uint4 w;
+              w.x = pack_bf16x2(o[8 * p] * st.x, o[8 * p + 1] * st.x);
+              w.y = pack_bf16x2(o[8 * p + 2] * st.x, o[8 * p + 3] * st.x);
+              w.z = pack_bf16x2(o[8 * p + 4] * st.x, o[8 * p + 5] * st.x);
+              w.w = pack_bf16x2(o[8 * p + 6] * st.x, o[8 * p + 7] * st.x);
+              if (!keys) w = make_uint4(0, 0, 0, 0);  // what TMEM holds then is old
+              *reinterpret_cast<uint4*>(mine + ((p ^ (lane & 7)) << 4)) = w;
+            }
             store_rows(static_cast<uint8_t*>(a.out) + c * 128, DH * 2);
           }
         } else {  // a share of the keys: O / l in fp32
