@@ -15,8 +15,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = ["api.cu", "route.cu", "attn.cu", "stga.cu", "shot.cu", "pipe.cu", "bwd.cu", "norm.cu", "cross.cu"]
-HEADERS = ["ptx.cuh", "internal.h", "windows.cuh"]
+SOURCES = ["api.cu", "route.cu", "attn.cu", "stga.cu", "shot.cu", "pipe.cu", "bwd.cu", "norm.cu", "cross.cu", "cross_bwd.cu"]
+HEADERS = ["ptx.cuh", "internal.h", "windows.cuh", "cross.cuh"]
 LIB = os.path.join(HERE, "libmoga.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -15,7 +15,8 @@
 //   query heads to a key head a tile holds 128 / r tokens of all r heads
 //   (one TMA box of 64 columns x r heads x 128 / r tokens), so that K and V are
 //   read once for all of them.
-//   warp 0  TMA of the K and V tiles (128 keys);  warp 3  TMA of the query tiles
+//   warp 0  TMA of the K and V tiles (128 keys)
+//   warp 3  walks the units and loads their query tiles
 //   warp 1  tcgen05.mma: PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); the next unit's
 //           first S follows its last PV without a gap
 //   warp 2  zeroes the rows of a V tile between the segment's last key and the
@@ -34,162 +35,17 @@
 
 #include <algorithm>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "cross.cuh"
 
 namespace moga {
 namespace {
 
-// Segments of a call, read from device memory and checked there.
-struct Seg {
-  int q0, q1, k0, k1;
-};
-__device__ __forceinline__ Seg segment(const CrossArgs& a, int s) {
-  Seg g;
-  g.q0 = a.q_off ? a.q_off[s] : 0;
-  g.q1 = a.q_off ? a.q_off[s + 1] : (int)a.N;
-  g.k0 = a.kv_off ? a.kv_off[s] : 0;
-  g.k1 = a.kv_off ? a.kv_off[s + 1] : (int)a.L;
-  if (a.kv_len) g.k1 = a.kv_len[s] < 0 || a.kv_len[s] > g.k1 - g.k0 ? -1 : g.k0 + a.kv_len[s];
-  return g;
-}
-// Offsets must rise from 0 or more to at most the rows there are, and a
-// length must fit its segment.  Every thread of the block gets the answer.
-__device__ bool segments_ok(const CrossArgs& a, int* status) {
-  bool bad = false;
-#pragma unroll 1
-  for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
-    const Seg g = segment(a, s);
-    bad |= g.q0 < 0 || g.q1 < g.q0 || g.q1 > a.N || g.k0 < 0 || g.k1 < g.k0 || g.k1 > a.L;
-    if (a.kv_off) bad |= a.kv_off[s + 1] < a.kv_off[s] || a.kv_off[s + 1] > a.L;
-  }
-  if (!__syncthreads_or(bad)) return true;
-  if (threadIdx.x == 0 && status) atomicOr(status, DEV_RANGE);
-  return false;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-  return v;
-}
-template <int C>
-__device__ __forceinline__ void load_row(const void* base, int64_t sn, int64_t sh, int64_t row, int h, int lane,
-                                         float (&x)[C]) {
-  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + row * sn + h * sh + lane * C;
-#pragma unroll
-  for (int i = 0; i < C; ++i) x[i] = __bfloat162float(p[i]);
-}
 template <int C>
 __device__ __forceinline__ void store_row(void* base, int64_t at, int lane, const float (&x)[C], float f) {
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at + lane * C;
 #pragma unroll
   for (int i = 0; i < C; ++i) p[i] = __float2bfloat16(x[i] * f);
 }
-template <int C>
-__device__ __forceinline__ float dot(const float (&x)[C], const float (&y)[C]) {
-  float v = 0.0f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) v = fmaf(x[i], y[i], v);
-  return warp_sum(v);
-}
-
-// One warp for each (query row, head): out and lse, or (kBwd) dq and D.
-template <int DH, bool kBwd>
-__global__ void __launch_bounds__(256) cross_rows_kernel(const CrossArgs a, int* status) {
-  constexpr int C = DH / 32;
-  if (!segments_ok(a, status)) return;
-  const int lane = threadIdx.x & 31;
-  const float scale = rsqrtf((float)DH);
-  const int64_t nw = (int64_t)gridDim.x * 8;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < a.N * a.H; w += nw) {
-    const int64_t n = w / a.H;
-    const int h = (int)(w - n * a.H), hk = h / (a.H / a.Hkv);
-    Seg g{0, 0, 0, 0};
-    for (int s = 0; s < a.S; ++s) {
-      const Seg t = segment(a, s);
-      if (n >= t.q0 && n < t.q1) g = t;
-    }
-    if (g.q1 <= g.q0) continue;  // a row of no segment
-    float q[C], o[C] = {}, k[C], v[C];
-    load_row<C>(a.q, a.q_sn, a.q_sh, n, h, lane, q);
-    const int64_t at = (n * a.H + h) * DH;
-    if (!kBwd) {
-      float m = -INFINITY, l = 0.0f;
-      for (int j = g.k0; j < g.k1; ++j) {
-        load_row<C>(a.k, a.k_sn, a.k_sh, j, hk, lane, k);
-        load_row<C>(a.v, a.v_sn, a.v_sh, j, hk, lane, v);
-        const float s = dot(q, k) * scale, mn = fmaxf(m, s);
-        const float f = expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = o[i] * f + p * v[i];
-      }
-      store_row<C>(a.out, at, lane, o, l > 0.0f ? 1.0f / l : 0.0f);
-      if (a.lse && lane == 0) a.lse[(int64_t)h * a.N + n] = m + logf(l);
-    } else {
-      float d[C], r[C], acc[C] = {};
-      load_row<C>(a.dout, (int64_t)a.H * DH, DH, n, h, lane, d);
-      load_row<C>(a.out, (int64_t)a.H * DH, DH, n, h, lane, r);
-      const float D = dot(d, r), lse = a.lse[(int64_t)h * a.N + n];
-      for (int j = g.k0; j < g.k1; ++j) {
-        load_row<C>(a.k, a.k_sn, a.k_sh, j, hk, lane, k);
-        load_row<C>(a.v, a.v_sn, a.v_sh, j, hk, lane, v);
-        const float ds = expf(dot(q, k) * scale - lse) * (dot(d, v) - D);
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
-      }
-      store_row<C>(a.dq, at, lane, acc, scale);
-      if (lane == 0) a.dsum[(int64_t)h * a.N + n] = D;
-    }
-  }
-}
-
-// One warp for each (key row, key head): dk and dv.
-template <int DH>
-__global__ void __launch_bounds__(256) cross_keys_kernel(const CrossArgs a, int* status) {
-  constexpr int C = DH / 32;
-  if (!segments_ok(a, status)) return;
-  const int lane = threadIdx.x & 31, share = a.H / a.Hkv;
-  const float scale = rsqrtf((float)DH);
-  const int64_t nw = (int64_t)gridDim.x * 8;
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < a.L * a.Hkv; w += nw) {
-    const int64_t j = w / a.Hkv;
-    const int hk = (int)(w - j * a.Hkv);
-    Seg g{0, 0, 0, 0};
-    for (int s = 0; s < a.S; ++s) {
-      const Seg t = segment(a, s);
-      if (j >= t.k0 && j < t.k1) g = t;
-    }
-    if (g.k1 <= g.k0) continue;
-    float k[C], v[C], q[C], d[C], dk[C] = {}, dv[C] = {};
-    load_row<C>(a.k, a.k_sn, a.k_sh, j, hk, lane, k);
-    load_row<C>(a.v, a.v_sn, a.v_sh, j, hk, lane, v);
-    for (int h = hk * share; h < (hk + 1) * share; ++h)
-      for (int n = g.q0; n < g.q1; ++n) {
-        load_row<C>(a.q, a.q_sn, a.q_sh, n, h, lane, q);
-        load_row<C>(a.dout, (int64_t)a.H * DH, DH, n, h, lane, d);
-        const int64_t i = (int64_t)h * a.N + n;
-        const float p = expf(dot(q, k) * scale - a.lse[i]), ds = p * (dot(d, v) - a.dsum[i]);
-#pragma unroll
-        for (int e = 0; e < C; ++e) {
-          dk[e] = fmaf(ds, q[e], dk[e]);
-          dv[e] = fmaf(p, d[e], dv[e]);
-        }
-      }
-    const int64_t at = (j * a.Hkv + hk) * DH;
-    store_row<C>(a.dk, at, lane, dk, scale);
-    store_row<C>(a.dv, at, lane, dv, 1.0f);
-  }
-}
-
-// ------------------------------------------------------------------ forward on the tensor cores
-constexpr int kXThreads = 512;
-constexpr int kMaxSeg = 1024;
-constexpr int kSplitSms = 148;  // a B200's SMs
-
-constexpr int kFeedSlots = 4;
-constexpr int kFeedReaders = 15;  // K/V, products, rows past the last key: a thread each; softmax and epilogue: 12 warps
 
 template <int DH>
 struct XPlan {
@@ -204,227 +60,10 @@ struct XPlan {
   static constexpr int kStat = kStage + 4 * 4096;    // [2 parities][2 tiles][128] of (1 / l, lse)
   static constexpr int kBar = kStat + 2 * 2 * kTile * 8;
   static constexpr int kFeed = kBar + 512;           // ring of units
-  static constexpr int kPre = kFeed + kFeedSlots * 32;  // units before each segment
-  static constexpr int kBytes = kPre + (kMaxSeg + 1) * 4 + 1024;
+  static constexpr int kBytes = kFeed + kFeedSlots * 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
 
-struct XUnit {
-  int g;               // key head, or query head without packing
-  int q0, q1;          // this unit's first token, its segment's end
-  int k0, k1;          // keys of this unit (its share of the segment's)
-  int split;
-};
-
-struct XGrid {
-  int tokens;          // tokens of a tile: 128 / r
-  int r, log2r;        // query heads of a tile
-  int splits;
-  int step_w, step_g;  // a step of gridDim.x units, in places and shares, and in heads
-};
-
-// The bounded wait of ptx.cuh, its loop out of line.  What runs here has to
-// fit the instruction cache: with that one inlined at some twenty places the
-// kernel had 114 KB of instructions, and a role's code was fetched anew each
-// time it came round (187,200 x 512 keys: 745 us; 613 us with 45 KB).
-template <int kSleep>
-__device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, const WaitCtx c) {
-  uint32_t n = 0, t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (kSleep > 0) __nanosleep(kSleep);
-    if (++n & 63u) continue;
-    const uint32_t t = (uint32_t)(global_timer_ns() >> 10);  // about a microsecond
-    if (n == 64) t0 = t;
-    if (t - t0 > (uint32_t)(c.limit_ns >> 10)) {
-      *c.abort_flag = 1;
-      if (c.status) atomicOr(c.status, DEV_TIMEOUT);
-    }
-    if (*c.abort_flag) return false;
-  }
-}
-template <int kSleep = 0>
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
-  return mbar_try_wait(bar, parity) || wait_more<kSleep>(smem_u32(bar), parity, c);
-}
-
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
-}
-
-// The products with descriptors of 128-byte swizzled operands (8-row groups
-// 1,024 bytes apart) given by their low words: the high word is a constant.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
-__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts_lo(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kDescHi)
-      : "memory");
-}
-
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok));
-  return ok != 0;
-}
-
-// mbar_try_wait without its suspension.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ int steps_of(const XUnit& u) { return (u.k1 - u.k0 + kTile - 1) / kTile; }
-
-// A CTA's units are blockIdx.x, then every gridDim.x-th, the heads of a place
-// next to one another (CTAs that run at once read whole token rows).  One
-// thread walks them, carrying head, place and segment along, and hands each
-// to the other roles through a ring in shared memory: with the walk in every
-// role the code that runs did not fit the instruction cache.
-struct Feed {
-  int4* ring;          // [kFeedSlots][2]: (g, q0, q1, split), (k0, k1, 1 or 0 at the end, -)
-  uint64_t* full;
-  uint64_t* empty;
-  uint32_t n;
-  // The next unit; false: none is left, or a wait gave up.  `warp`: all of a
-  // warp's threads read, and its first one frees the slot.
-  template <bool kWarp, int kSleep = 0>
-  __device__ __forceinline__ bool next(XUnit& u, const WaitCtx& wc) {
-    const uint32_t s = n % kFeedSlots;
-    if (!wait_for<kSleep>(&full[s], (n / kFeedSlots) & 1, wc)) return false;
-    const int4 a = ring[2 * s], b = ring[2 * s + 1];
-    if (kWarp) __syncwarp();
-    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&empty[s]);
-    ++n;
-    u = XUnit{a.x, a.y, a.z, b.x, b.y, a.w};
-    return b.z != 0;
-  }
-  __device__ __forceinline__ bool put(const XUnit& u, int more, const WaitCtx& wc) {
-    const uint32_t s = n % kFeedSlots;
-    if (!wait_for(&empty[s], ((n / kFeedSlots) & 1) ^ 1, wc)) return false;
-    ring[2 * s] = make_int4(u.g, u.q0, u.q1, u.split);
-    ring[2 * s + 1] = make_int4(u.k0, u.k1, more, 0);
-    mbar_arrive(&full[s]);
-    ++n;
-    return true;
-  }
-};
-
-struct Walk {
-  const CrossArgs& a;
-  const XGrid& x;
-  const int* pre;
-  int heads;           // units of a place: one per key head, or per query head without packing
-  int left;            // units to come
-  int g, w, s;         // head; place and share; segment
-  Seg seg;
-  __device__ __forceinline__ Walk(const CrossArgs& a_, const XGrid& x_, const int* pre_) : a(a_), x(x_), pre(pre_) {
-    heads = a.H >> x.log2r;
-    const int total = pre[a.S] * x.splits * heads;
-    left = (int)blockIdx.x < total ? (total - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
-    w = (int)blockIdx.x / heads;
-    g = (int)blockIdx.x - w * heads;
-    s = 0;
-    seg = segment(a, 0);
-  }
-  __device__ __forceinline__ bool next(XUnit& u) {
-    if (left-- <= 0) return false;
-    int p = w;
-    u.split = 0;
-    if (x.splits > 1) {
-      p = (int)((unsigned)w / (unsigned)x.splits);
-      u.split = w - p * x.splits;
-    }
-    if (p >= pre[s + 1]) {  // some segments have no place
-#pragma unroll 1
-      do ++s; while (p >= pre[s + 1]);
-      seg = segment(a, s);
-    }
-    u.g = g;
-    u.q0 = seg.q0 + (p - pre[s]) * 2 * x.tokens;
-    u.q1 = seg.q1;
-    u.k0 = seg.k0;
-    u.k1 = seg.k1;
-    if (x.splits > 1) {
-      const unsigned n = (unsigned)(seg.k1 - seg.k0 + kTile - 1) / kTile, each = n / (unsigned)x.splits,
-                     over = n - each * (unsigned)x.splits;  // the first `over` shares have one tile more
-      const unsigned t0 = each * (unsigned)u.split + min((unsigned)u.split, over);
-      u.k0 = seg.k0 + (int)(t0 * kTile);
-      u.k1 = min(seg.k1, u.k0 + (int)((each + ((unsigned)u.split < over ? 1u : 0u)) * kTile));
-    }
-    w += x.step_w;
-    g += x.step_g;
-    if (g >= heads) {
-      g -= heads;
-      ++w;
-    }
-    return true;
-  }
-};
-
-// pre[s] = places (pairs of query tiles) before segment s.
-__device__ void place_table(const CrossArgs& a, int per_place, int* pre) {
-  int run = 0;
-#pragma unroll 1
-  for (int base = 0; base < a.S; base += 32) {  // warp 0 alone: S / 32 rounds
-    if (threadIdx.x < 32) {
-      const int s = base + (int)threadIdx.x;
-      int n = 0;
-      if (s < a.S) {
-        const Seg g = segment(a, s);
-        n = (g.q1 - g.q0 + per_place - 1) / per_place;
-      }
-      int sum = n;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, sum, m);
-        if ((int)threadIdx.x >= m) sum += t;
-      }
-      if (s < a.S) pre[s] = run + sum - n;
-      run += __shfl_sync(0xffffffffu, sum, 31);
-    }
-  }
-  if (threadIdx.x == 0) pre[a.S] = run;
-}
-
-// Head h's rows in a 2-D view of a [n, heads, d_h] tensor: column h * x + c,
-// row h * y + token (token-major: y = 0; head-major: x = 0).
-struct XView {
-  int x, y;
-};
 
 struct XMaps {
   CUtensorMap q, k, v;
@@ -458,7 +97,6 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(done_bar + 2);
   static_assert(16 + 5 * P::kStages + 2 * kFeedSlots + 3 <= 64, "barrier area holds 64 words");
-  int* pre = reinterpret_cast<int*>(smem + P::kPre);
   float2* stat = reinterpret_cast<float2*>(smem + P::kStat);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -489,7 +127,6 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     *abort_flag = 0;
     fence_mbar_init();
   }
-  place_table(a, 2 * xg.tokens, pre);
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -509,13 +146,15 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
   if (warp < 4) {
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- K and V tiles
-      tma_prefetch_desc(&m.k);
-      tma_prefetch_desc(&m.v);
+      if (a.L > 0) {
+        tma_prefetch_desc(&m.k);
+        tma_prefetch_desc(&m.v);
+      }
       const uint64_t keep = l2_policy_evict_last();
       uint32_t t = 0;
       bool ok = true, kv_pending = false;  // kv_pending: the last K has no V behind it
       while (ok && feed.next<false>(u, wc)) {
-        const int n = steps_of(u);
+        const int n = ((u.k1 - u.k0 + kTile - 1) / kTile);
         const int hk = xg.r > 1 ? u.g : u.g / share;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
@@ -524,18 +163,10 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           const int row = u.k0 + j * kTile;
           if (!wait_for(&k_empty[s], ph, wc)) { ok = false; break; }
           if (withhold && t == 0) { ok = false; break; }  // test hook: this tile never comes
-          mbar_expect_tx(&k_full[s], P::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < P::kChunks; ++c)
-            tma_load_2d_hint(&m.k, &k_full[s], smem + P::kK + s * P::kTileBytes + c * P::kChunk, hk * m.kv.x + c * 64,
-                             hk * m.kv.y + row, keep);
+          load_tile<DH>(&m.k, m.kv, &k_full[s], smem + P::kK + s * P::kTileBytes, 1, hk, row, keep);
           kv_pending = true;
           if (!wait_for(&v_empty[s], ph, wc)) { ok = false; break; }
-          mbar_expect_tx(&v_full[s], P::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < P::kChunks; ++c)
-            tma_load_2d_hint(&m.v, &v_full[s], smem + P::kV + s * P::kTileBytes + c * P::kChunk, hk * m.vv.x + c * 64,
-                             hk * m.vv.y + row, keep);
+          load_tile<DH>(&m.v, m.vv, &v_full[s], smem + P::kV + s * P::kTileBytes, 1, hk, row, keep);
           kv_pending = false;
           ++t;
         }
@@ -548,38 +179,42 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         if (s < tk) wait_for(&k_full[s], ((tk - 1 - s) / P::kStages) & 1, dc);
         if (s < t) wait_for(&v_full[s], ((t - 1 - s) / P::kStages) & 1, dc);
       }
-    } else if (warp == 3 && lane == 0) {
+    } else if (warp == 3) {
       // -------------------------------------------------------------- units, and their query tiles
-      tma_prefetch_desc(&m.q);
+      if (lane == 0) tma_prefetch_desc(&m.q);
       const uint64_t once = l2_policy_evict_first();
-      uint32_t n[2] = {0, 0};
-      bool ok = true;
-      Walk it(a, xg, pre);
-      while (ok) {
-        const bool more = it.next(u);
-        if (!feed.put(u, more ? 1 : 0, wc) || !more) break;
-        if (steps_of(u) == 0) continue;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int tok = u.q0 + x * xg.tokens;
-          if (tok >= u.q1) break;
-          if (!wait_for(&q_empty[x], (n[x] & 1) ^ 1, wc)) { ok = false; break; }
-          mbar_expect_tx(&q_full[x], P::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < P::kChunks; ++c) {
-            uint8_t* dst = smem + P::kQ + x * P::kTileBytes + c * P::kChunk;
-            if (xg.r > 1)
-              tma_load_3d(&m.q, &q_full[x], dst, c * 64, u.g * xg.r, tok);
-            else
-              tma_load_2d_hint(&m.q, &q_full[x], dst, u.g * m.qv.x + c * 64, u.g * m.qv.y + tok, once);
+      uint32_t n0 = 0, n1 = 0;  // tiles A, B loaded
+      Walk it(a, xg, 2 * xg.tokens, false);
+      while (true) {
+        int place;
+        const bool more = it.next(u, place);
+        u.q0 += place * 2 * xg.tokens;
+        take_share(u.k0, u.k1, kTile, u.split, xg.splits);
+        int go = 1;
+        if (lane == 0) {
+          go = feed.put(u, more ? 1 : 0, wc);
+          if (go && more && u.k1 > u.k0) {
+            const int head = u.g << xg.log2r;
+            go = wait_for(&q_empty[0], (n0 & 1) ^ 1, wc);
+            if (go) {
+              load_tile<DH>(&m.q, m.qv, &q_full[0], smem + P::kQ, xg.r, head, u.q0, once);
+              ++n0;
+            }
+            if (go && u.q0 + xg.tokens < u.q1) {
+              go = wait_for(&q_empty[1], (n1 & 1) ^ 1, wc);
+              if (go) {
+                load_tile<DH>(&m.q, m.qv, &q_full[1], smem + P::kQ + P::kTileBytes, xg.r, head, u.q0 + xg.tokens, once);
+                ++n1;
+              }
+            }
           }
-          ++n[x];
         }
+        if (!__shfl_sync(0xffffffffu, go, 0) || !more) break;
       }
       volatile int zero = 0;
       WaitCtx dc{&zero, nullptr, 100000000ull};
-      for (int x = 0; x < 2; ++x)
-        if (n[x] > 0) wait_for(&q_full[x], (n[x] - 1) & 1, dc);
+      if (lane == 0 && n0 > 0) wait_for(&q_full[0], (n0 - 1) & 1, dc);
+      if (lane == 0 && n1 > 0) wait_for(&q_full[1], (n1 - 1) & 1, dc);
     } else if (warp == 2) {
       // -------------------------------------------------------------- rows past the last key
       uint32_t t = 0;
@@ -597,18 +232,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           if (lane == 0) w = wait_for(&v_full[s], (t / P::kStages) & 1, wc);
           if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
           __syncwarp();
-          const int valid = keys - j * kTile;
-          if (valid < kTile) {
-            const int end = min((valid + 15) & ~15, kTile);
-            uint8_t* v = smem + P::kV + s * P::kTileBytes;
-#pragma unroll 1
-            for (int i = lane; i < (end - valid) * 8 * P::kChunks; i += 32) {
-              const int piece = i & 7, c = (i >> 3) % P::kChunks, r = valid + (i >> 3) / P::kChunks;
-              *reinterpret_cast<uint4*>(v + c * P::kChunk + r * 128 + piece * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          zero_rows<DH>(smem + P::kV + s * P::kTileBytes, keys - j * kTile, lane);
           if (lane == 0) mbar_arrive(&v_ready[s]);
         }
       }
@@ -716,7 +340,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           ++j;
         } else {
           u = nu;
-          n = steps_of(u);
+          n = ((u.k1 - u.k0 + kTile - 1) / kTile);
           j = 0;
           have = next;
         }
@@ -735,7 +359,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     uint32_t sc = 0, un = 0;
     bool ok = true;
     while (ok && feed.next<true>(u, wc)) {
-      const int n = steps_of(u);
+      const int n = ((u.k1 - u.k0 + kTile - 1) / kTile);
       if (n == 0 || u.q0 + x * xg.tokens >= u.q1) continue;
       float m_run = -INFINITY;
       uint64_t l2 = f2_pack(0.f, 0.f);
@@ -858,7 +482,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     uint32_t un0 = 0, un1 = 0;  // units of tile A, B
     bool ok = true;
     while (ok && feed.next<true, 100>(u, wc)) {
-      const bool keys = steps_of(u) > 0;
+      const bool keys = u.k1 > u.k0;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
         const int tok0 = u.q0 + x * xg.tokens;
@@ -990,44 +614,18 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
   if (a.lse && lane == 0) a.lse[at] = m + logf(l);
 }
 
-// 2-D view of a [n, heads, d_h] tensor whose box is 64 columns x 128 tokens of a head.
-bool view_2d(CUtensorMap* map, XView* v, const void* base, int64_t sn, int64_t sh, int64_t n, int H, int d_h) {
-  if (n == 0) return true;  // nothing is read through it
-  if (H == 1 || sn >= (H - 1) * sh + d_h) {  // token-major
-    *v = XView{(int)sh, 0};
-    return make_tmap_2d(map, base, (uint64_t)((H - 1) * sh + d_h), (uint64_t)n, (uint64_t)sn * 2, kTile);
-  }
-  *v = XView{0, (int)(sh / sn)};
-  return make_tmap_2d(map, base, (uint64_t)d_h, (uint64_t)(H - 1) * (sh / sn) + n, (uint64_t)sn * 2, kTile);
-}
-
-// Query heads of a tile: all that share a key head, where they are a power of
-// two up to 64 and q is token-major with a token stride in whole head strides.
-int pack_of(const CrossArgs& a) {
-  const int r = a.H / a.Hkv;
-  if (r < 2 || r > 64 || (r & (r - 1))) return 1;
-  return a.q_sn >= (a.H - 1) * a.q_sh + a.d_h && a.q_sn % a.q_sh == 0 ? r : 1;
-}
-
-// Places (pairs of query tiles) of a call, at most: each segment may add a ragged one.
-int64_t places_most(int64_t N, int r, int S) { return N == 0 ? 0 : ceil_div(N, 2 * kTile / r) + std::min<int64_t>(S, N) - 1; }
 
 // Shares of the keys: enough units for every SM, each of two key tiles at least.
 int splits_of(int64_t N, int64_t L, int H, int r, int S) {
-  const int64_t units = places_most(N, r, S) * (H / r);
-  if (units == 0 || units >= kSplitSms) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kSplitSms / units, ceil_div(ceil_div(L, S), 2 * kTile)));
+  return shares(places_most(N, 2 * kTile / r, S) * (H / r), ceil_div(L, S), kTile, kSplitSms);
 }
 
 template <int DH>
 cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches) {
   using P = XPlan<DH>;
   XMaps m{};
-  XGrid x;
-  x.r = pack_of(a);
-  x.log2r = 0;
-  while (1 << x.log2r < x.r) ++x.log2r;
-  x.tokens = kTile / x.r;
+  XGrid x = pack_grid(pack_of(a));
+  x.heads = a.H / x.r;
   x.splits = splits_of(a.N, a.L, a.H, x.r, a.S);
   bool ok = view_2d(&m.k, &m.kv, a.k, a.k_sn, a.k_sh, a.L, a.Hkv, DH) &&
             view_2d(&m.v, &m.vv, a.v, a.v_sn, a.v_sh, a.L, a.Hkv, DH);
@@ -1041,10 +639,9 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
   }
   cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t units = places_most(a.N, x.r, a.S) * x.splits * (a.H / x.r);
+  const int64_t units = places_most(a.N, 2 * x.tokens, a.S) * x.splits * x.heads;
   const unsigned grid = (unsigned)std::min<int64_t>(units, c.num_sms);
-  x.step_w = (int)grid / (a.H / x.r);
-  x.step_g = (int)grid % (a.H / x.r);
+  set_steps(&x, grid);
   cross_fwd_kernel<DH><<<grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, po, pl, a.withhold, c.status,
                                                                  (unsigned long long)c.wait_ns);
   *launches = 1;
@@ -1052,11 +649,6 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
   cross_join_kernel<DH><<<(unsigned)ceil_div(a.N * a.H, 8), 256, 0, c.stream>>>(a, x.splits, po, pl, c.status);
   *launches = 2;
   return cudaGetLastError();
-}
-
-unsigned blocks_for(const DevCtx& c, int64_t warps) {
-  const int64_t b = ceil_div(warps, 8), cap = (int64_t)c.num_sms * 64;
-  return (unsigned)(b < cap ? b : cap);
 }
 
 }  // namespace
@@ -1071,30 +663,11 @@ size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S)
   }
   return most;
 }
-size_t cross_bwd_ws_bytes(int64_t N, int64_t, int H, int, int, int) { return (size_t)N * H * 4; }
 
 cudaError_t launch_cross_attn(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches) {
   *launches = 0;
   if (a.N == 0) return cudaSuccess;
   return a.d_h == 128 ? launch_fwd<128>(c, a, ws, launches) : launch_fwd<64>(c, a, ws, launches);
-}
-
-cudaError_t launch_cross_bwd(const DevCtx& c, const CrossArgs& args, uint8_t* ws, int* launches) {
-  CrossArgs a = args;
-  a.dsum = reinterpret_cast<float*>(ws);
-  *launches = 0;
-  if (a.N > 0) {
-    (a.d_h == 128 ? cross_rows_kernel<128, true> : cross_rows_kernel<64, true>)<<<blocks_for(c, a.N * a.H), 256, 0, c.stream>>>(a, c.status);
-    ++*launches;
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (a.L > 0) {
-    (a.d_h == 128 ? cross_keys_kernel<128> : cross_keys_kernel<64>)<<<blocks_for(c, a.L * a.Hkv), 256, 0, c.stream>>>(a, c.status);
-    ++*launches;
-    return cudaGetLastError();
-  }
-  return cudaSuccess;
 }
 
 }  // namespace moga

@@ -1,0 +1,971 @@
+// Gradients of cross attention (the forward and its conventions are in
+// cross.cu).  With P = exp(S - lse), dP = dO V^T, D = rowsum(dO * O) and
+// dS = P * (dP - D):
+//   dQ = dS K / sqrt(d_h),   dK = dS^T Q / sqrt(d_h),   dV = P^T dO.
+//
+// Two passes, each with S and dP anew: 14 instead of 10 flops per pair and
+// channel.  One pass would have to add every key tile's share of dQ, 64 KB of
+// fp32 for a tile of each kind, outside the SM: more bytes than the products
+// saved, in an order that changes.
+//
+// cross_dq_kernel   a unit is one 128-row query tile (rows as in the forward:
+//   128 / r tokens of r heads) and its segment's keys.  Per key tile t:
+//   dP(t), dQ(t - 1), S(t + 1), across units: queries have two slots, so that a
+//   prompt of a few tiles leaves no gap between one unit and the next.
+// cross_dkv_kernel  a unit is one 128-row key tile of a key head and a share of
+//   its segment's queries, over the query heads that share the key head.  Per
+//   query tile t: S^T(t), dV and dK (t - 1), dP^T(t).  Prompts have few key
+//   tiles (512 keys of 12 heads: 48 for 148 SMs), so the queries are split and
+//   the shares' fp32 sums added by cross_sum_kernel in a fixed order.
+//
+// Warp 0 loads K and V (dQ) or Q and dO (dK, dV), warp 3 the stationary tiles
+// of the units it walks, warp 1 issues the products, warp 2 zeroes rows past
+// a segment's end (and brings lse and D of the query rows), warps 4-11 turn S
+// and dP into bf16 P and dS (two warpgroups, 64 columns each) in the TMEM
+// columns that S had, which the closing products read as their A operand;
+// warps 12-15 write the results and, for dQ, compute D a unit ahead.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cross.cuh"
+
+namespace moga {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct BMaps {
+  CUtensorMap q, dout, k, v;
+  XView qv, dv, kv, vv;
+};
+
+template <int DH>
+struct BPlan {
+  static constexpr int T = kTile * DH * 2;        // bytes of a tile
+  static constexpr int kChunk = kTile * 128;
+  // dQ: queries (two units), dO, K ring of three, V.  K is read by S and, a
+  // tile later, by dQ; V by dP alone.
+  static constexpr int kQ = 0, kDO = 2 * T, kK = 3 * T, kV = 6 * T;
+  // dK, dV: K, V, query ring of three, dO ring of two.
+  static constexpr int kX1 = 0, kX2 = T, kY1 = 2 * T, kY2 = 5 * T;
+  static constexpr int kVec = 7 * T;              // fp32 vectors (dQ: 2 KB; dK, dV: 2.5 KB)
+  static constexpr int kFeed = kVec + 5 * kTile * 4;
+  static constexpr int kBar = kFeed + kFeedSlots * 32;
+  static constexpr int kBytes = kBar + 384;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+
+// The dynamic shared memory of a kernel without static shared memory starts
+// on a 1 KB boundary; the tiles need it and there is no room to move them.
+__device__ __forceinline__ bool base_ok(const uint8_t* smem, int* status) {
+  if ((smem_u32(smem) & 1023u) == 0) return true;
+  if (threadIdx.x == 0 && status) atomicOr(status, DEV_RANGE);
+  return false;
+}
+
+// A tile's 128 x 128 product of two K-major operands into TMEM.
+template <int DH>
+__device__ __forceinline__ void issue_nt(uint32_t d, uint32_t a_lo, uint32_t b_lo) {
+  constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+  for (int kk = 0; kk < DH / 16; ++kk) {
+    const uint32_t o = ((kk >> 2) * kTile * 128 + (kk & 3) * 32) >> 4;
+    umma_lo(d, a_lo + o, b_lo + o, id, (uint32_t)kk);
+  }
+}
+// d += A B over `valid` rows of B in steps of 16: A in TMEM, where warpgroup w
+// wrote rows [64 w, 64 w + 64) of B as 32 columns from 64 w; B MN-major.
+template <int DH>
+__device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a_tmem, uint32_t b_lo, int valid, bool acc) {
+  constexpr uint32_t id = idesc_bf16(128, DH, false, true);
+  if (valid >= kTile) {
+#pragma unroll
+    for (int kk = 0; kk < kTile / 16; ++kk)
+      umma_ts_lo(d, a_tmem + 64 * (kk >> 2) + 8 * (kk & 3), b_lo + kk * 128, id, (acc || kk > 0) ? 1u : 0u);
+  } else {
+#pragma unroll 1
+    for (int kk = 0; kk * 16 < valid; ++kk)
+      umma_ts_lo(d, a_tmem + 64 * (kk >> 2) + 8 * (kk & 3), b_lo + kk * 128, id, (acc || kk > 0) ? 1u : 0u);
+  }
+}
+
+// One row of DH accumulators, scaled: bf16 to `out`, or fp32 to `part`.
+template <int DH>
+__device__ __forceinline__ void write_row(uint32_t taddr, float f, bool keep, bool live, __nv_bfloat16* out,
+                                          float* part) {
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    float o[32];
+    __syncwarp();
+    tmem_ld32(taddr + c, o);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = keep ? o[e] * f : 0.0f;
+    if (live && part) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4*>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    } else if (live) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        *reinterpret_cast<uint4*>(out + c + e) =
+            make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
+                       pack_bf16x2(o[e + 6], o[e + 7]));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dQ
+template <int DH>
+__global__ void __launch_bounds__(kXThreads, 1)
+cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid xg, float* part, int* status,
+                unsigned long long wait_ns) {
+  using P = BPlan<DH>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!base_ok(smem, status) || !segments_ok(a, status)) return;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
+  uint64_t* q_full = bars;            // [2]: by unit
+  uint64_t* q_empty = bars + 2;       // [2]
+  uint64_t* do_full = bars + 4;
+  uint64_t* do_empty = bars + 5;
+  uint64_t* k_full = bars + 6;        // [3]
+  uint64_t* k_ready = bars + 9;       // [3]: rows past the last key zeroed
+  uint64_t* k_empty = bars + 12;      // [3]
+  uint64_t* v_full = bars + 15;
+  uint64_t* v_ready = bars + 16;
+  uint64_t* v_empty = bars + 17;
+  uint64_t* s_full = bars + 18;       // [2]: S of tile t on t % 2
+  uint64_t* d_full = bars + 20;       // dP computed
+  uint64_t* dp_free = bars + 21;      // dP read
+  uint64_t* p_full = bars + 22;       // [2]: dS of tile t written
+  uint64_t* acc_full = bars + 24;
+  uint64_t* acc_empty = bars + 25;
+  uint64_t* vec_full = bars + 26;     // [2]: lse and D of a unit's rows
+  uint64_t* f_full = bars + 28;       // [4]
+  uint64_t* f_empty = bars + 32;      // [4]
+  uint64_t* sum_bar = bars + 36;      // a row's two halves of D added
+  uint64_t* done_bar = bars + 37;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 38);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 39);
+  float* vec = reinterpret_cast<float*>(smem + P::kVec);  // [2 units][-lse log2 e, D][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 38; ++i) {
+      const bool all = i == 21 || i == 22 || i == 23 || i == 36, epi = i == 25 || i == 26 || i == 27, feed = i >= 32 && i < 36;
+      mbar_init(&bars[i], all ? 256 : epi ? 128 : feed ? kFeedReaders : 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM: S (then dS over it) of tile t at 0 or 384, dP at 128, dQ at 256
+  auto tS = [tmem](uint32_t t) { return tmem + ((t & 1u) ? 384u : 0u); };
+  const uint32_t tD = tmem + 128u, tQ = tmem + 256u;
+  WaitCtx wc{abort_flag, status, wait_ns};
+  Feed feed{reinterpret_cast<int4*>(smem + P::kFeed), f_full, f_empty, 0};
+  XUnit u{};
+  const int share = a.H / a.Hkv;
+  volatile int zero = 0;
+  WaitCtx dc{&zero, nullptr, 100000000ull};  // for loads and products in flight at the end
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- K, one tile ahead of V
+      const uint64_t keep = l2_policy_evict_last();
+      uint32_t kt = 0, vt = 0;
+      bool ok = true;
+      auto load_v = [&](int head, int row) {
+        ok = wait_for(v_empty, (vt & 1) ^ 1, wc);
+        if (!ok) return;
+        load_tile<DH>(&m.v, m.vv, v_full, smem + P::kV, 1, head, row, keep);
+        ++vt;
+      };
+      int vh = 0, vr = 0;
+      while (ok && feed.next<false>(u, wc)) {
+        const int hk = xg.r > 1 ? u.g : u.g / share;
+#pragma unroll 1
+        for (int row = u.k0; row < u.k1 && ok; row += kTile) {
+          const uint32_t s = kt % 3;
+          ok = wait_for(&k_empty[s], ((kt / 3) & 1) ^ 1, wc);
+          if (!ok) break;
+          load_tile<DH>(&m.k, m.kv, &k_full[s], smem + P::kK + s * P::T, 1, hk, row, keep);
+          if (kt++ > 0) load_v(vh, vr);
+          vh = hk;
+          vr = row;
+        }
+      }
+      if (ok && kt > vt) load_v(vh, vr);
+      for (uint32_t s = 0; s < 3; ++s)
+        if (s < kt) wait_for(&k_full[s], ((kt - 1 - s) / 3) & 1, dc);
+      if (vt > 0) wait_for(v_full, (vt - 1) & 1, dc);
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- units, their Q and dO tiles
+    const uint64_t once = l2_policy_evict_first();
+    uint32_t n = 0, nd = 0;
+    Walk it(a, xg, xg.tokens, false);
+    while (true) {
+      int place;
+      const bool more = it.next(u, place);
+      u.q0 += place * xg.tokens;
+      const bool whole = u.k1 - u.k0 <= kTile;  // the unit's one tile holds its segment's keys
+      take_share(u.k0, u.k1, kTile, u.split, xg.splits);
+      int go = 1;
+      if (lane == 0) {
+        // bit 1 of the entry's flag: D comes from P and dP (see below)
+        go = feed.put(u, more ? (whole && xg.splits == 1 ? 3 : 1) : 0, wc);
+        if (go && more && u.k1 > u.k0) {
+          const int head = u.g << xg.log2r;
+          const uint32_t s = n & 1;
+          go = wait_for(&q_empty[s], ((n >> 1) & 1) ^ 1, wc);
+          if (go) {
+            load_tile<DH>(&m.q, m.qv, &q_full[s], smem + P::kQ + s * P::T, xg.r, head, u.q0, once);
+            ++n;
+            go = wait_for(do_empty, (nd & 1) ^ 1, wc);
+          }
+          if (go) {
+            load_tile<DH>(&m.dout, m.dv, do_full, smem + P::kDO, xg.r, head, u.q0, once);
+            ++nd;
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, go, 0) || !more) break;
+    }
+    if (lane == 0) {
+      for (uint32_t s = 0; s < 2; ++s)
+        if (s < n) wait_for(&q_full[s], ((n - 1 - s) >> 1) & 1, dc);
+      if (nd > 0) wait_for(do_full, (nd - 1) & 1, dc);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- rows past the last key
+    uint32_t t = 0;
+    bool ok = true;
+    while (ok) {
+      int w = 1;
+      if (lane == 0) w = feed.next<false>(u, wc);
+      if (!__shfl_sync(0xffffffffu, w, 0)) break;
+      const int keys = __shfl_sync(0xffffffffu, u.k1 - u.k0, 0);
+#pragma unroll 1
+      for (int j = 0; j * kTile < keys; ++j, ++t) {
+        const uint32_t s = t % 3;
+        if (lane == 0) w = wait_for(&k_full[s], (t / 3) & 1, wc);
+        if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+        __syncwarp();
+        zero_rows<DH>(smem + P::kK + s * P::T, keys - j * kTile, lane);
+        if (lane == 0) {
+          mbar_arrive(&k_ready[s]);
+          w = wait_for(v_full, t & 1, wc);
+        }
+        if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+        __syncwarp();
+        zero_rows<DH>(smem + P::kV, keys - j * kTile, lane);
+        if (lane == 0) mbar_arrive(v_ready);
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    const bool leader = elect_one();
+    const uint32_t q_lo = desc_lo(smem_u32(smem + P::kQ), 16), do_lo = desc_lo(smem_u32(smem + P::kDO), 16),
+                   k_lo = desc_lo(smem_u32(smem + P::kK), 16), kt_lo = desc_lo(smem_u32(smem + P::kK), P::kChunk),
+                   v_lo = desc_lo(smem_u32(smem + P::kV), 16);
+    XUnit nu{};
+    bool left = true, have = false;      // units may be left; there is a unit
+    int n = 0, j = 0;                    // its tiles, and this one
+    uint32_t t = 0, un = 0;              // tiles and units so far (this one not)
+    int wait_valid = 0;                  // keys of tile t - 1, whose dQ is open (0: none)
+    bool wait_first = false, wait_last = false;
+    uint32_t accs = 0;                   // units whose dQ has begun
+    while (true) {
+      bool ok = true;
+      const bool more = have && j + 1 < n;
+      if (have) {
+        // dP(t)
+        ok = wait_for(v_ready, t & 1, wc) && (j > 0 || wait_for(do_full, un & 1, wc)) &&
+             (t == 0 || wait_for(dp_free, (t - 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          issue_nt<DH>(tD, do_lo, v_lo);
+          umma_commit(d_full);
+          umma_commit(v_empty);
+          if (!more) umma_commit(do_empty);
+        }
+      }
+      if (wait_valid > 0) {
+        // dQ(t - 1)
+        const uint32_t tp = t - 1;
+        ok = wait_for(&p_full[tp & 1], (tp >> 1) & 1, wc);
+        if (ok && wait_first) {
+          if (accs > 0) ok = wait_for(acc_empty, (accs - 1) & 1, wc);
+          ++accs;
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          issue_acc<DH>(tQ, tS(tp), kt_lo + (tp % 3) * (P::T >> 4), wait_valid, !wait_first);
+          umma_commit(&k_empty[tp % 3]);
+          if (wait_last) umma_commit(acc_full);
+        }
+        wait_valid = 0;
+      }
+      // S of the next tile
+      bool next = more;
+      if (!more)
+        while (left && !next) {
+          left = feed.next<true>(nu, wc);
+          next = left && nu.k1 > nu.k0;
+        }
+      const uint32_t t1 = have ? t + 1 : 0, un1 = more ? un : have ? un + 1 : 0;
+      if (next) {
+        ok = wait_for(&k_ready[t1 % 3], (t1 / 3) & 1, wc) && (more || wait_for(&q_full[un1 & 1], (un1 >> 1) & 1, wc));
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          issue_nt<DH>(tS(t1), q_lo + (un1 & 1) * (P::T >> 4), k_lo + (t1 % 3) * (P::T >> 4));
+          umma_commit(&s_full[t1 & 1]);
+          if (more ? j + 2 == n : nu.k1 - nu.k0 <= kTile) umma_commit(&q_empty[un1 & 1]);  // the unit's last S
+        }
+      }
+      if (!have && !next) break;
+      if (have) {
+        wait_valid = min(u.k1 - u.k0 - j * kTile, kTile);
+        wait_first = j == 0;
+        wait_last = !more;
+      }
+      if (more) {
+        ++j;
+      } else {
+        u = nu;
+        n = (u.k1 - u.k0 + kTile - 1) / kTile;
+        j = 0;
+        have = next;
+      }
+      t = t1;
+      un = un1;
+    }
+    if (leader) umma_commit(done_bar);
+    wait_for(done_bar, 0, dc);
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- dS
+    const int wg = (warp - 4) >> 2, sub = warp & 3, row = sub * 32 + lane;
+    const uint32_t at = ((uint32_t)(sub * 32) << 16) + 64 * wg;  // this warp's lanes, its warpgroup's columns
+    const float scale_log2 = kLog2e * rsqrtf((float)DH);
+    uint32_t t = 0, un = 0, sums = 0;
+    bool ok = true;
+    int flag;
+    while (ok && (flag = feed.next_flag<true>(u, wc)) != 0) {
+      if (u.k1 <= u.k0) continue;
+      float* mine = vec + (un & 1) * 2 * kTile + row;
+      if (!wait_for(&vec_full[un & 1], (un >> 1) & 1, wc)) break;
+      const float nl = mine[0];
+      float D = mine[kTile];
+#pragma unroll 1
+      for (int k = u.k0; k < u.k1; k += kTile, ++t) {
+        if (!wait_for(&s_full[t & 1], (t >> 1) & 1, wc)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t ts = tS(t) + at;
+        float p[64];
+        tmem_ld32(ts, p);
+        tmem_ld32(ts + 32, p + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 64; ++e) p[e] = fast_exp2(fmaf(p[e], scale_log2, nl));
+        const int valid = u.k1 - k - 64 * wg;
+        if (valid < 64) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) p[e] = e < valid ? p[e] : 0.0f;
+        }
+        if (!wait_for(d_full, t & 1, wc)) { ok = false; break; }
+        tc_fence_after();
+        if (flag & 2) {
+          // One tile holds all of the row's keys: D = sum_j P_ij dP_ij, in
+          // fp32.  From O, which is rounded to bf16, it would be the largest
+          // error of the gradients where few keys make O as large as V.
+          float sum = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            float d[32];
+            tmem_ld32(tD + at + c, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float pe = c ? p[32 + e] : p[e];
+              if (c + e < valid) sum = fmaf(pe, d[e], sum);
+            }
+          }
+          atomicAdd(mine + kTile, sum);  // 0 and two terms: the same in either order
+          mbar_arrive(sum_bar);
+          ok = wait_for(sum_bar, sums & 1, wc);
+          if (!ok) break;
+          ++sums;
+          D = mine[kTile];
+          const int tok = u.q0 + (row >> xg.log2r);
+          if (wg == 0 && tok < u.q1)
+            a.dsum[(int64_t)((u.g << xg.log2r) + (row & (xg.r - 1))) * a.N + tok] = D;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float d[32];
+          tmem_ld32(tD + at + 32 * c, d);
+          tmem_ld_wait();
+          if (c == 1) {
+            tc_fence_before();
+            mbar_arrive(dp_free);
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            pk[e] = pack_bf16x2(p[32 * c + 2 * e] * (d[2 * e] - D), p[32 * c + 2 * e + 1] * (d[2 * e + 1] - D));
+          tmem_st16u(ts + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t & 1]);
+      }
+      ++un;
+    }
+  } else {
+    // ---------------------------------------------------------------- D a unit ahead, and the results
+    const int sub = warp & 3, row = sub * 32 + lane;
+    const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+    constexpr int LPR = DH / 8, RPW = 32 / LPR;
+    uint32_t un = 0, on = 0;
+    XUnit pu{};
+    bool pending = false, ok = true;
+    auto write = [&](const XUnit& w, bool keys) {
+      const int tok = w.q0 + (row >> xg.log2r), h = (w.g << xg.log2r) + (row & (xg.r - 1));
+      const bool live = tok < w.q1;
+      const int64_t o = live ? ((int64_t)tok * a.H + h) * DH : 0;
+      write_row<DH>(tQ + lanes, rsqrtf((float)DH), keys, live, static_cast<__nv_bfloat16*>(a.dq) + o,
+                    part ? part + (int64_t)w.split * a.N * a.H * DH + o : nullptr);
+    };
+    auto finish = [&]() {  // the unit before
+      if (!wait_for<100>(acc_full, on & 1, wc)) return false;
+      ++on;
+      tc_fence_after();
+      write(pu, true);
+      tc_fence_before();
+      mbar_arrive(acc_empty);
+      return true;
+    };
+    int flag;
+    while (ok && (flag = feed.next_flag<true, 100>(u, wc)) != 0) {
+      const bool keys = u.k1 > u.k0;
+      if (keys) {
+        float* out = vec + (un & 1) * 2 * kTile;
+        const int tok = u.q0 + (row >> xg.log2r), h = (u.g << xg.log2r) + (row & (xg.r - 1));
+        out[row] = tok < u.q1 ? -a.lse[(int64_t)h * a.N + tok] * kLog2e : -INFINITY;
+        out[kTile + row] = 0.0f;
+        __syncwarp();
+        if (!(flag & 2)) {
+          const int l = lane % LPR;
+#pragma unroll 4
+          for (int i = 0; i < 32; i += RPW) {
+            const int r = sub * 32 + i + lane / LPR;
+            const int tk = u.q0 + (r >> xg.log2r), hh = (u.g << xg.log2r) + (r & (xg.r - 1));
+            float s = 0.0f;
+            if (tk < u.q1) {
+              const int64_t o = ((int64_t)tk * a.H + hh) * DH + l * 8;
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + o));
+              const uint4 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + o));
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+                s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+              }
+            }
+#pragma unroll
+            for (int k = LPR / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+            if (l == 0) {
+              out[kTile + r] = s;
+              if (u.split == 0 && tk < u.q1) a.dsum[(int64_t)hh * a.N + tk] = s;
+            }
+          }
+        }
+        mbar_arrive(&vec_full[un & 1]);
+        ++un;
+      }
+      if (pending) ok = finish();
+      pending = keys;
+      if (keys) pu = u; else write(u, false);
+    }
+    if (ok && pending) finish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+template <int DH>
+__global__ void __launch_bounds__(kXThreads, 1)
+cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid xg, float* part, int* status,
+                 unsigned long long wait_ns) {
+  using P = BPlan<DH>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (!base_ok(smem, status) || !segments_ok(a, status)) return;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
+  uint64_t* x_full = bars;
+  uint64_t* x_empty = bars + 1;
+  uint64_t* y1_full = bars + 2;       // [3]: Q
+  uint64_t* y1_ready = bars + 5;      // [3]: rows past the last query zeroed, lse there
+  uint64_t* y1_empty = bars + 8;      // [3]
+  uint64_t* y2_full = bars + 11;      // [2]: dO
+  uint64_t* y2_ready = bars + 13;     // [2]: likewise, with D
+  uint64_t* y2_empty = bars + 15;     // [2]
+  uint64_t* s_full = bars + 17;
+  uint64_t* d_full = bars + 18;
+  uint64_t* dp_free = bars + 19;
+  uint64_t* p_full = bars + 20;       // [2]
+  uint64_t* acc_full = bars + 22;
+  uint64_t* acc_empty = bars + 23;
+  uint64_t* f_full = bars + 24;       // [4]
+  uint64_t* f_empty = bars + 28;      // [4]
+  uint64_t* done_bar = bars + 32;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 34);
+  float* vec1 = reinterpret_cast<float*>(smem + P::kVec);  // [3][128]: -lse log2 e
+  float* vec2 = vec1 + 3 * kTile;                          // [2][128]: D
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 33; ++i) {
+      const bool all = i == 19 || i == 20 || i == 21, feed = i >= 28 && i < 32;
+      mbar_init(&bars[i], all ? 256 : i == 23 ? 128 : feed ? kFeedReaders : 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM: S^T of tile t (then P, and dS 32 columns on) in buffer t % 2 of two,
+  // dP^T in the other; dV at 256, dK behind it.
+  auto tS = [tmem](uint32_t t) { return tmem + 128u * (t & 1u); };
+  auto tD = [tmem](uint32_t t) { return tmem + 128u * ((t & 1u) ^ 1u); };
+  const uint32_t tV = tmem + 256u, tK = tmem + 256u + (uint32_t)DH;
+  WaitCtx wc{abort_flag, status, wait_ns};
+  Feed feed{reinterpret_cast<int4*>(smem + P::kFeed), f_full, f_empty, 0};
+  XUnit u{};
+  // A unit's query tiles: [q0, q1) in steps of xg.tokens, once, or (without
+  // packing) once for every query head that shares the key head.
+  const int loops = xg.r > 1 ? 1 : a.H / a.Hkv;
+  const int share = a.H / a.Hkv;
+  auto head_of = [&](int g, int loop) { return g * share + loop; };
+  volatile int zero = 0;
+  WaitCtx dc{&zero, nullptr, 100000000ull};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- Q and dO
+      const uint64_t keep = l2_policy_evict_last();
+      uint32_t t1 = 0, t2 = 0;
+      bool ok = true;
+      while (ok && feed.next<false>(u, wc)) {
+#pragma unroll 1
+        for (int loop = 0; loop < loops && ok; ++loop) {
+          const int h = head_of(u.g, loop);
+#pragma unroll 1
+          for (int tok = u.q0; tok < u.q1; tok += xg.tokens) {
+            const uint32_t s1 = t1 % 3, s2 = t2 % 2;
+            if (!wait_for(&y1_empty[s1], ((t1 / 3) & 1) ^ 1, wc)) { ok = false; break; }
+            load_tile<DH>(&m.q, m.qv, &y1_full[s1], smem + P::kY1 + s1 * P::T, xg.r, h, tok, keep);
+            ++t1;
+            if (!wait_for(&y2_empty[s2], ((t2 / 2) & 1) ^ 1, wc)) { ok = false; break; }
+            load_tile<DH>(&m.dout, m.dv, &y2_full[s2], smem + P::kY2 + s2 * P::T, xg.r, h, tok, keep);
+            ++t2;
+          }
+        }
+      }
+      for (uint32_t s = 0; s < 3; ++s)
+        if (s < t1) wait_for(&y1_full[s], ((t1 - 1 - s) / 3) & 1, dc);
+      for (uint32_t s = 0; s < 2; ++s)
+        if (s < t2) wait_for(&y2_full[s], ((t2 - 1 - s) / 2) & 1, dc);
+    }
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------- units, their K and V tiles
+    const uint64_t once = l2_policy_evict_first();
+    uint32_t n = 0;
+    Walk it(a, xg, kTile, true);
+    while (true) {
+      int place;
+      const bool more = it.next(u, place);
+      u.k0 += place * kTile;
+      take_share(u.q0, u.q1, xg.tokens, u.split, xg.splits);
+      int go = 1;
+      if (lane == 0) {
+        go = feed.put(u, more ? 1 : 0, wc);
+        if (go && more && u.q1 > u.q0) {
+          go = wait_for(x_empty, (n & 1) ^ 1, wc);
+          if (go) {
+            // both tiles on one barrier: the second's bytes are added before the first phase can complete
+            mbar_expect_tx(x_full, 2 * P::T);
+#pragma unroll
+            for (int c = 0; c < DH / 64; ++c) {
+              tma_load_2d_hint(&m.k, x_full, smem + P::kX1 + c * P::kChunk, u.g * m.kv.x + c * 64, u.g * m.kv.y + u.k0, once);
+              tma_load_2d_hint(&m.v, x_full, smem + P::kX2 + c * P::kChunk, u.g * m.vv.x + c * 64, u.g * m.vv.y + u.k0, once);
+            }
+            ++n;
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, go, 0) || !more) break;
+    }
+    if (lane == 0 && n > 0) wait_for(x_full, (n - 1) & 1, dc);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------------- rows past the last query; lse and D
+    uint32_t t = 0;
+    bool ok = true;
+    while (ok) {
+      int w = 1;
+      if (lane == 0) w = feed.next<false>(u, wc);
+      if (!__shfl_sync(0xffffffffu, w, 0)) break;
+      const int q0 = __shfl_sync(0xffffffffu, u.q0, 0), q1 = __shfl_sync(0xffffffffu, u.q1, 0),
+                g = __shfl_sync(0xffffffffu, u.g, 0);
+#pragma unroll 1
+      for (int loop = 0; loop < loops && ok; ++loop) {
+#pragma unroll 1
+        for (int tok0 = q0; tok0 < q1; tok0 += xg.tokens, ++t) {
+          const uint32_t s1 = t % 3, s2 = t % 2;
+          const int valid = min(q1 - tok0, xg.tokens) << xg.log2r;
+          float lv[4], dv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = lane + 32 * i;
+            const int64_t at = (int64_t)(head_of(g, loop) + (r & (xg.r - 1))) * a.N + tok0 + (r >> xg.log2r);
+            lv[i] = r < valid ? -a.lse[at] * kLog2e : -INFINITY;
+            dv[i] = r < valid ? a.dsum[at] : 0.0f;
+          }
+          if (lane == 0) w = wait_for(&y1_full[s1], (t / 3) & 1, wc);
+          if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+          __syncwarp();
+          zero_rows<DH>(smem + P::kY1 + s1 * P::T, valid, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vec1[s1 * kTile + lane + 32 * i] = lv[i];
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&y1_ready[s1]);
+            w = wait_for(&y2_full[s2], (t / 2) & 1, wc);
+          }
+          if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
+          __syncwarp();
+          zero_rows<DH>(smem + P::kY2 + s2 * P::T, valid, lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vec2[s2 * kTile + lane + 32 * i] = dv[i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&y2_ready[s2]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- products
+    const bool leader = elect_one();
+    const uint32_t x1_lo = desc_lo(smem_u32(smem + P::kX1), 16), x2_lo = desc_lo(smem_u32(smem + P::kX2), 16),
+                   y1_lo = desc_lo(smem_u32(smem + P::kY1), 16), y2_lo = desc_lo(smem_u32(smem + P::kY2), 16),
+                   y1t_lo = desc_lo(smem_u32(smem + P::kY1), P::kChunk), y2t_lo = desc_lo(smem_u32(smem + P::kY2), P::kChunk);
+    uint32_t t = 0, un = 0;
+    bool ok = true;
+    while (ok && feed.next<true>(u, wc)) {
+      if (u.q1 <= u.q0) continue;
+      const int per = (u.q1 - u.q0 + xg.tokens - 1) / xg.tokens, n = per * loops;
+      if (!wait_for(x_full, un & 1, wc)) break;
+      int left = u.q1 - u.q0, open = 0;  // tokens from this tile on in its loop; rows of tile t - 1 (0: none)
+#pragma unroll 1
+      for (int j = 0; j <= n; ++j) {
+        if (j < n) {
+          // S^T(t) goes where dP^T(t - 1) was
+          ok = wait_for(&y1_ready[t % 3], (t / 3) & 1, wc) && (t == 0 || wait_for(dp_free, (t - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            issue_nt<DH>(tS(t), x1_lo, y1_lo + (t % 3) * (P::T >> 4));
+            umma_commit(s_full);
+          }
+        }
+        if (open > 0) {
+          // dV and dK of tile t - 1
+          const uint32_t tp = t - 1;
+          ok = wait_for(&p_full[tp & 1], (tp >> 1) & 1, wc) && (j > 1 || un == 0 || wait_for(acc_empty, (un - 1) & 1, wc));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            issue_acc<DH>(tV, tS(tp), y2t_lo + (tp % 2) * (P::T >> 4), open, j > 1);
+            issue_acc<DH>(tK, tS(tp) + 32, y1t_lo + (tp % 3) * (P::T >> 4), open, j > 1);
+            umma_commit(&y1_empty[tp % 3]);
+            umma_commit(&y2_empty[tp % 2]);
+            if (j == n) umma_commit(acc_full);
+          }
+        }
+        if (j < n) {
+          // dP^T(t) goes where dV and dK of tile t - 1 read P and dS
+          ok = wait_for(&y2_ready[t % 2], (t / 2) & 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            issue_nt<DH>(tD(t), x2_lo, y2_lo + (t % 2) * (P::T >> 4));
+            umma_commit(d_full);
+            if (j + 1 == n) umma_commit(x_empty);
+          }
+          open = min(left, xg.tokens) << xg.log2r;
+          left -= xg.tokens;
+          if (left <= 0) left = u.q1 - u.q0;
+          ++t;
+        }
+      }
+      ++un;
+    }
+    if (leader) umma_commit(done_bar);
+    wait_for(done_bar, 0, dc);
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- P and dS
+    const int wg = (warp - 4) >> 2, sub = warp & 3;
+    const uint32_t at = ((uint32_t)(sub * 32) << 16) + 64 * wg;
+    const float scale_log2 = kLog2e * rsqrtf((float)DH);
+    uint32_t t = 0;
+    bool ok = true;
+    while (ok && feed.next<true>(u, wc)) {
+      const int n = u.q1 > u.q0 ? (u.q1 - u.q0 + xg.tokens - 1) / xg.tokens * loops : 0;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j, ++t) {
+        ok = wait_for(s_full, t & 1, wc) && wait_for(&y1_ready[t % 3], (t / 3) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ts = tS(t) + at;
+        const float4* nl = reinterpret_cast<const float4*>(vec1 + (t % 3) * kTile + 64 * wg);
+        float p[64];
+        tmem_ld32(ts, p);
+        tmem_ld32(ts + 32, p + 32);
+        tmem_ld_wait();
+        // Columns past the last query: zeroed rows of Q and -inf make P 0.
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float4 v = nl[e];
+          p[4 * e] = fast_exp2(fmaf(p[4 * e], scale_log2, v.x));
+          p[4 * e + 1] = fast_exp2(fmaf(p[4 * e + 1], scale_log2, v.y));
+          p[4 * e + 2] = fast_exp2(fmaf(p[4 * e + 2], scale_log2, v.z));
+          p[4 * e + 3] = fast_exp2(fmaf(p[4 * e + 3], scale_log2, v.w));
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[32 * c + 2 * e], p[32 * c + 2 * e + 1]);
+          tmem_st16u(ts + 16 * c, pk);
+        }
+        ok = wait_for(d_full, t & 1, wc) && wait_for(&y2_ready[t % 2], (t / 2) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        const float4* dd = reinterpret_cast<const float4*>(vec2 + (t % 2) * kTile + 64 * wg);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float d[32];
+          tmem_ld32(tD(t) + at + 32 * c, d);
+          tmem_ld_wait();
+          if (c == 1) {
+            tc_fence_before();
+            mbar_arrive(dp_free);
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = dd[8 * c + e];
+            const float* q = p + 32 * c + 4 * e;
+            pk[2 * e] = pack_bf16x2(q[0] * (d[4 * e] - v.x), q[1] * (d[4 * e + 1] - v.y));
+            pk[2 * e + 1] = pack_bf16x2(q[2] * (d[4 * e + 2] - v.z), q[3] * (d[4 * e + 3] - v.w));
+          }
+          tmem_st16u(ts + 32 + 16 * c, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t & 1]);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- the results
+    const int sub = warp & 3, row = sub * 32 + lane;
+    const uint32_t lanes = (uint32_t)(sub * 32) << 16;
+    const int64_t rows = a.L * a.Hkv;
+    uint32_t on = 0;
+    while (feed.next<true, 500>(u, wc)) {
+      const bool some = u.q1 > u.q0;
+      if (some) {
+        if (!wait_for<500>(acc_full, on & 1, wc)) break;
+        ++on;
+        tc_fence_after();
+      }
+      const int key = u.k0 + row;
+      const bool live = key < u.k1;
+      const int64_t o = live ? ((int64_t)key * a.Hkv + u.g) * DH : 0;
+      float* pv = part ? part + ((int64_t)u.split * 2 * rows) * DH + o : nullptr;
+      write_row<DH>(tV + lanes, 1.0f, some, live, static_cast<__nv_bfloat16*>(a.dv) + o, pv);
+      write_row<DH>(tK + lanes, rsqrtf((float)DH), some, live, static_cast<__nv_bfloat16*>(a.dk) + o,
+                    part ? pv + rows * DH : nullptr);
+      if (some) {
+        tc_fence_before();
+        mbar_arrive(acc_empty);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// out = the sum of the shares' rows, for rows of a segment: `keys` rows are
+// [L, H_kv] and part holds two tensors per share, others [N, H] and one.
+template <int DH>
+__global__ void __launch_bounds__(256) cross_sum_kernel(const CrossArgs a, bool keys, int splits,
+                                                        const float* __restrict__ part, int64_t step,
+                                                        __nv_bfloat16* __restrict__ out) {
+  if (!segments_ok(a, nullptr)) return;
+  const int heads = keys ? a.Hkv : a.H;
+  const int64_t rows = (keys ? a.L : a.N) * heads;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * (DH / 8)) return;
+  const int64_t row = i / (DH / 8) / heads;
+  bool inside = true;
+  if (!keys) {
+    if (a.q_off) inside = row >= a.q_off[0] && row < a.q_off[a.S];
+  } else if (a.kv_off || a.kv_len) {
+    int lo = 0, hi = a.S - 1;  // the last segment that starts at or before the row and is not empty before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (segment(a, mid).k0 <= row) lo = mid; else hi = mid - 1;
+    }
+    const Seg s = segment(a, lo);
+    inside = row >= s.k0 && row < s.k1;
+  }
+  if (!inside) return;
+  float v[8] = {};
+#pragma unroll 2
+  for (int s = 0; s < splits; ++s) {
+    const float4* p = reinterpret_cast<const float4*>(part + s * step + i * 8);
+    const float4 x = p[0], y = p[1];
+    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+  }
+  reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Shares of the keys for dQ, as in the forward, and of the queries for dK and
+// dV: four rounds of units on every SM, so that the last one's ragged end
+// costs little.
+int dq_splits(int64_t N, int64_t L, int H, int r, int S) {
+  return shares(places_most(N, kTile / r, S) * (H / r), ceil_div(L, S), kTile, kSplitSms);
+}
+int dkv_splits(int64_t N, int64_t L, int H_kv, int r, int S) {
+  return shares(places_most(L, kTile, S) * H_kv, ceil_div(N, S), kTile / r, 4 * kSplitSms);
+}
+
+struct BwdWs {
+  size_t dsum, dq, dkv, total;
+};
+BwdWs bwd_ws(int64_t N, int64_t L, int H, int H_kv, int d_h, int S, int r) {
+  BwdWs w{};
+  const int nq = dq_splits(N, L, H, r, S), nk = dkv_splits(N, L, H_kv, r, S);
+  w.dq = align_up((size_t)N * H * 4, 256);
+  w.dkv = w.dq + align_up(nq > 1 ? (size_t)nq * N * H * d_h * 4 : 0, 256);
+  w.total = w.dkv + (nk > 1 ? (size_t)nk * 2 * L * H_kv * d_h * 4 : 0);
+  return w;
+}
+
+template <int DH>
+cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches) {
+  using P = BPlan<DH>;
+  BMaps m{};
+  const int r = pack_of(a);
+  const int64_t HD = (int64_t)a.H * DH;
+  const XGrid base = pack_grid(r);
+  const BwdWs w = bwd_ws(a.N, a.L, a.H, a.Hkv, DH, a.S, r);
+  a.dsum = reinterpret_cast<float*>(ws + w.dsum);
+  bool ok = view_2d(&m.k, &m.kv, a.k, a.k_sn, a.k_sh, a.L, a.Hkv, DH) &&
+            view_2d(&m.v, &m.vv, a.v, a.v_sn, a.v_sh, a.L, a.Hkv, DH);
+  if (r > 1)
+    ok = ok && make_tmap_heads(&m.q, a.q, DH, a.H, a.N, a.q_sh, a.q_sn, r, base.tokens) &&
+         make_tmap_heads(&m.dout, a.dout, DH, a.H, a.N, DH, HD, r, base.tokens);
+  else
+    ok = ok && view_2d(&m.q, &m.qv, a.q, a.q_sn, a.q_sh, a.N, a.H, DH) &&
+         view_2d(&m.dout, &m.dv, a.dout, HD, DH, a.N, a.H, DH);
+  if (!ok) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if ((e = cudaFuncSetAttribute(cross_dq_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(cross_dkv_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess)
+    return e;
+  auto sum = [&](bool keys, int splits, const float* part, int64_t step, void* out) {
+    const int64_t n = (keys ? a.L * a.Hkv : a.N * a.H) * (DH / 8);
+    cross_sum_kernel<DH><<<(unsigned)ceil_div(n, 256), 256, 0, c.stream>>>(a, keys, splits, part, step,
+                                                                         static_cast<__nv_bfloat16*>(out));
+    ++*launches;
+    return cudaGetLastError();
+  };
+  if (a.N > 0) {
+    XGrid x = base;
+    x.heads = a.H / r;
+    x.splits = dq_splits(a.N, a.L, a.H, r, a.S);
+    float* part = x.splits > 1 ? reinterpret_cast<float*>(ws + w.dq) : nullptr;
+    const int64_t grid = std::min<int64_t>(places_most(a.N, x.tokens, a.S) * x.heads * x.splits, c.num_sms);
+    set_steps(&x, grid);
+    cross_dq_kernel<DH><<<(unsigned)grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, part, c.status,
+                                                                          (unsigned long long)c.wait_ns);
+    ++*launches;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (part && (e = sum(false, x.splits, part, a.N * HD, a.dq)) != cudaSuccess) return e;
+  }
+  if (a.L > 0) {
+    XGrid x = base;
+    x.heads = a.Hkv;
+    x.splits = dkv_splits(a.N, a.L, a.Hkv, r, a.S);
+    float* part = x.splits > 1 ? reinterpret_cast<float*>(ws + w.dkv) : nullptr;
+    const int64_t grid = std::min<int64_t>(places_most(a.L, kTile, a.S) * x.heads * x.splits, c.num_sms);
+    set_steps(&x, grid);
+    cross_dkv_kernel<DH><<<(unsigned)grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, part, c.status,
+                                                                           (unsigned long long)c.wait_ns);
+    ++*launches;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t kd = a.L * a.Hkv * DH;
+    if (part && ((e = sum(true, x.splits, part, 2 * kd, a.dv)) != cudaSuccess ||
+                 (e = sum(true, x.splits, part + kd, 2 * kd, a.dk)) != cudaSuccess))
+      return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t cross_bwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S) {
+  // Packed or not is known with the strides only: the larger of the two.
+  size_t most = 0;
+  for (int r : {1, H / H_kv}) {
+    if (r < 1 || r > 64 || (r & (r - 1))) continue;
+    most = std::max(most, bwd_ws(N, L, H, H_kv, d_h, S, r).total);
+  }
+  return most;
+}
+
+cudaError_t launch_cross_bwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* launches) {
+  *launches = 0;
+  return a.d_h == 128 ? launch_bwd<128>(c, a, ws, launches) : launch_bwd<64>(c, a, ws, launches);
+}
+
+}  // namespace moga
