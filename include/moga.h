@@ -452,6 +452,8 @@ moga_status moga_cross_attn(const void* q, int64_t q_stride_n, int64_t q_stride_
  *      summed over the query heads that share a key head.  Rows of no segment
  *      (and key rows past a segment's length) are left as they were.  All sums
  *      are taken in a fixed order.
+ * dout, out, dq, dk, dv and ws are 32-byte aligned (whole sectors are read and
+ * written).
  * Workspace: moga_cross_attn_backward_workspace_size(...) bytes. */
 size_t moga_cross_attn_backward_workspace_size(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
 moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_stride_n, int64_t q_stride_h,

@@ -818,7 +818,10 @@ class CrossAttnFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         q, k, v, out, lse, *seg = ctx.saved_tensors
-        g = cross_attn_backward(dout.to(torch.bfloat16).contiguous(), q, k, v, out, lse, *seg)
+        dout = dout.to(torch.bfloat16).contiguous()
+        if dout.data_ptr() % 32:
+            dout = dout.clone()
+        g = cross_attn_backward(dout, q, k, v, out, lse, *seg)
         return g["dq"], g["dk"], g["dv"], None, None, None
 
 

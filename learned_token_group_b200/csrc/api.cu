@@ -108,6 +108,7 @@ uint8_t* noalloc_scratch(int dev) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr size_t kHeader = 256;  // status word and spare words
@@ -1314,8 +1315,8 @@ moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_
                                     kv_offsets, kv_lens, S);
   if (st != MOGA_OK) return st;
   if ((N > 0 && (!dout || !out || !lse || !dq)) || (L > 0 && (!dk || !dv))) return MOGA_ERR_INVALID_ARG;
-  if (!aligned16(dout) || !aligned16(out) || !aligned4(lse) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
-      !ws || !aligned16(ws))
+  if (!aligned32(dout) || !aligned32(out) || !aligned4(lse) || !aligned32(dq) || !aligned32(dk) || !aligned32(dv) ||
+      !ws || !aligned32(ws))
     return MOGA_ERR_INVALID_ARG;
   if (ws_bytes < moga_cross_attn_backward_workspace_size(N, L, H, H_kv, d_h, S)) return MOGA_ERR_WORKSPACE;
   DevCtx c;

@@ -278,6 +278,22 @@ __device__ __forceinline__ void load_tile(const CUtensorMap* map, const XView& v
   }
 }
 
+// The same tile into L2.
+template <int DH>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, const XView& v, int r, int head, int row) {
+#pragma unroll
+  for (int c = 0; c < DH / 64; ++c) {
+    if (r > 1)
+      asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(c * 64),
+                   "r"(head), "r"(row)
+                   : "memory");
+    else
+      asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map),
+                   "r"(head * v.x + c * 64), "r"(head * v.y + row)
+                   : "memory");
+  }
+}
+
 // Zeroes rows [valid, next multiple of 16) of a tile (a whole warp).  Products
 // run in steps of 16 rows, and what a row of another segment or past the last
 // one holds may be NaN, of which 0 times is NaN.

@@ -10,8 +10,8 @@
 //
 // cross_dq_kernel   a unit is one 128-row query tile (rows as in the forward:
 //   128 / r tokens of r heads) and its segment's keys.  Per key tile t:
-//   dP(t), dQ(t - 1), S(t + 1), across units: queries have two slots, so that a
-//   prompt of a few tiles leaves no gap between one unit and the next.
+//   dP(t), dQ(t - 1), S(t + 1), across units, so that a prompt of a few tiles
+//   leaves no gap between one unit and the next.
 // cross_dkv_kernel  a unit is one 128-row key tile of a key head and a share of
 //   its segment's queries, over the query heads that share the key head.  Per
 //   query tile t: S^T(t), dV and dK (t - 1), dP^T(t).  Prompts have few key
@@ -37,17 +37,18 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BMaps {
-  CUtensorMap q, dout, k, v;
-  XView qv, dv, kv, vv;
+  CUtensorMap q, dout, out, k, v;
+  XView qv, dv, kv, vv;  // out is laid out as dout
 };
 
 template <int DH>
 struct BPlan {
   static constexpr int T = kTile * DH * 2;        // bytes of a tile
   static constexpr int kChunk = kTile * 128;
-  // dQ: queries (two units), dO, K ring of three, V.  K is read by S and, a
-  // tile later, by dQ; V by dP alone.
-  static constexpr int kQ = 0, kDO = 2 * T, kK = 3 * T, kV = 6 * T;
+  // dQ: Q, dO, K ring of three, V ring of two.  K is read by S and, a tile
+  // later, by dQ; V by dP alone.  S of a unit's last tile is issued a tile
+  // ahead, so the next unit's Q has a tile's time to come.
+  static constexpr int kQ = 0, kDO = T, kK = 2 * T, kV = 5 * T;
   // dK, dV: K, V, query ring of three, dO ring of two.
   static constexpr int kX1 = 0, kX2 = T, kY1 = 2 * T, kY2 = 5 * T;
   static constexpr int kVec = 7 * T;              // fp32 vectors (dQ: 2 KB; dK, dV: 2.5 KB)
@@ -91,6 +92,20 @@ __device__ __forceinline__ void issue_acc(uint32_t d, uint32_t a_tmem, uint32_t 
   }
 }
 
+// A whole 32-byte sector: each thread writes its own row, so that a store of
+// 16 bytes would touch every sector twice.
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+__device__ __forceinline__ void load32(uint32_t* w, const void* p) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+
 // One row of DH accumulators, scaled: bf16 to `out`, or fp32 to `part`.
 template <int DH>
 __device__ __forceinline__ void write_row(uint32_t taddr, float f, bool keep, bool live, __nv_bfloat16* out,
@@ -105,14 +120,15 @@ __device__ __forceinline__ void write_row(uint32_t taddr, float f, bool keep, bo
     for (int e = 0; e < 32; ++e) o[e] = keep ? o[e] * f : 0.0f;
     if (live && part) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4)
-        *reinterpret_cast<float4*>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      for (int e = 0; e < 32; e += 8) store32(part + c + e, reinterpret_cast<const uint32_t*>(o + e));
     } else if (live) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 8)
-        *reinterpret_cast<uint4*>(out + c + e) =
-            make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
-                       pack_bf16x2(o[e + 6], o[e + 7]));
+      for (int e = 0; e < 32; e += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[e + 2 * i], o[e + 2 * i + 1]);
+        store32(out + c + e, w);
+      }
     }
   }
 }
@@ -126,18 +142,18 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
   extern __shared__ __align__(1024) uint8_t smem[];
   if (!base_ok(smem, status) || !segments_ok(a, status)) return;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
-  uint64_t* q_full = bars;            // [2]: by unit
-  uint64_t* q_empty = bars + 2;       // [2]
-  uint64_t* do_full = bars + 4;
-  uint64_t* do_empty = bars + 5;
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* do_full = bars + 2;
+  uint64_t* do_empty = bars + 3;
   uint64_t* k_full = bars + 6;        // [3]
   uint64_t* k_ready = bars + 9;       // [3]: rows past the last key zeroed
   uint64_t* k_empty = bars + 12;      // [3]
-  uint64_t* v_full = bars + 15;
-  uint64_t* v_ready = bars + 16;
-  uint64_t* v_empty = bars + 17;
-  uint64_t* s_full = bars + 18;       // [2]: S of tile t on t % 2
-  uint64_t* d_full = bars + 20;       // dP computed
+  uint64_t* v_full = bars + 15;       // [2]
+  uint64_t* v_ready = bars + 4;       // [2]
+  uint64_t* v_empty = bars + 17;      // [2]
+  uint64_t* s_full = bars + 19;       // [2]: S of tile t on t % 2
+  uint64_t* d_full = bars + 38;       // dP computed
   uint64_t* dp_free = bars + 21;      // dP read
   uint64_t* p_full = bars + 22;       // [2]: dS of tile t written
   uint64_t* acc_full = bars + 24;
@@ -147,12 +163,12 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
   uint64_t* f_empty = bars + 32;      // [4]
   uint64_t* sum_bar = bars + 36;      // a row's two halves of D added
   uint64_t* done_bar = bars + 37;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 38);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 39);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 39);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 40);
   float* vec = reinterpret_cast<float*>(smem + P::kVec);  // [2 units][-lse log2 e, D][128]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 38; ++i) {
+    for (int i = 0; i < 39; ++i) {
       const bool all = i == 21 || i == 22 || i == 23 || i == 36, epi = i == 25 || i == 26 || i == 27, feed = i >= 32 && i < 36;
       mbar_init(&bars[i], all ? 256 : epi ? 128 : feed ? kFeedReaders : 1);
     }
@@ -179,34 +195,27 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
 
   if (warp == 0) {
     if (lane == 0) {
-      // -------------------------------------------------------------- K, one tile ahead of V
+      // -------------------------------------------------------------- K and V
       const uint64_t keep = l2_policy_evict_last();
       uint32_t kt = 0, vt = 0;
       bool ok = true;
-      auto load_v = [&](int head, int row) {
-        ok = wait_for(v_empty, (vt & 1) ^ 1, wc);
-        if (!ok) return;
-        load_tile<DH>(&m.v, m.vv, v_full, smem + P::kV, 1, head, row, keep);
-        ++vt;
-      };
-      int vh = 0, vr = 0;
       while (ok && feed.next<false>(u, wc)) {
         const int hk = xg.r > 1 ? u.g : u.g / share;
 #pragma unroll 1
-        for (int row = u.k0; row < u.k1 && ok; row += kTile) {
-          const uint32_t s = kt % 3;
-          ok = wait_for(&k_empty[s], ((kt / 3) & 1) ^ 1, wc);
-          if (!ok) break;
+        for (int row = u.k0; row < u.k1; row += kTile) {
+          const uint32_t s = kt % 3, sv = vt % 2;
+          if (!wait_for(&k_empty[s], ((kt / 3) & 1) ^ 1, wc)) { ok = false; break; }
           load_tile<DH>(&m.k, m.kv, &k_full[s], smem + P::kK + s * P::T, 1, hk, row, keep);
-          if (kt++ > 0) load_v(vh, vr);
-          vh = hk;
-          vr = row;
+          ++kt;
+          if (!wait_for(&v_empty[sv], ((vt / 2) & 1) ^ 1, wc)) { ok = false; break; }
+          load_tile<DH>(&m.v, m.vv, &v_full[sv], smem + P::kV + sv * P::T, 1, hk, row, keep);
+          ++vt;
         }
       }
-      if (ok && kt > vt) load_v(vh, vr);
       for (uint32_t s = 0; s < 3; ++s)
         if (s < kt) wait_for(&k_full[s], ((kt - 1 - s) / 3) & 1, dc);
-      if (vt > 0) wait_for(v_full, (vt - 1) & 1, dc);
+      for (uint32_t s = 0; s < 2; ++s)
+        if (s < vt) wait_for(&v_full[s], ((vt - 1 - s) / 2) & 1, dc);
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- units, their Q and dO tiles
@@ -222,13 +231,17 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       int go = 1;
       if (lane == 0) {
         // bit 1 of the entry's flag: D comes from P and dP (see below)
-        go = feed.put(u, more ? (whole && xg.splits == 1 ? 3 : 1) : 0, wc);
+        const int flag = more ? (whole && xg.splits == 1 ? 3 : 1) : 0;
+        const int head = u.g << xg.log2r;
+        if (flag == 1 && u.k1 > u.k0) {  // what D is computed from, a unit ahead
+          prefetch_tile<DH>(&m.out, m.dv, xg.r, head, u.q0);
+          prefetch_tile<DH>(&m.dout, m.dv, xg.r, head, u.q0);
+        }
+        go = feed.put(u, flag, wc);
         if (go && more && u.k1 > u.k0) {
-          const int head = u.g << xg.log2r;
-          const uint32_t s = n & 1;
-          go = wait_for(&q_empty[s], ((n >> 1) & 1) ^ 1, wc);
+          go = wait_for(q_empty, (n & 1) ^ 1, wc);
           if (go) {
-            load_tile<DH>(&m.q, m.qv, &q_full[s], smem + P::kQ + s * P::T, xg.r, head, u.q0, once);
+            load_tile<DH>(&m.q, m.qv, q_full, smem + P::kQ, xg.r, head, u.q0, once);
             ++n;
             go = wait_for(do_empty, (nd & 1) ^ 1, wc);
           }
@@ -241,8 +254,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       if (!__shfl_sync(0xffffffffu, go, 0) || !more) break;
     }
     if (lane == 0) {
-      for (uint32_t s = 0; s < 2; ++s)
-        if (s < n) wait_for(&q_full[s], ((n - 1 - s) >> 1) & 1, dc);
+      if (n > 0) wait_for(q_full, (n - 1) & 1, dc);
       if (nd > 0) wait_for(do_full, (nd - 1) & 1, dc);
     }
   } else if (warp == 2) {
@@ -263,12 +275,12 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
         zero_rows<DH>(smem + P::kK + s * P::T, keys - j * kTile, lane);
         if (lane == 0) {
           mbar_arrive(&k_ready[s]);
-          w = wait_for(v_full, t & 1, wc);
+          w = wait_for(&v_full[t % 2], (t / 2) & 1, wc);
         }
         if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
         __syncwarp();
-        zero_rows<DH>(smem + P::kV, keys - j * kTile, lane);
-        if (lane == 0) mbar_arrive(v_ready);
+        zero_rows<DH>(smem + P::kV + (t % 2) * P::T, keys - j * kTile, lane);
+        if (lane == 0) mbar_arrive(&v_ready[t % 2]);
       }
     }
   } else if (warp == 1) {
@@ -289,14 +301,14 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       const bool more = have && j + 1 < n;
       if (have) {
         // dP(t)
-        ok = wait_for(v_ready, t & 1, wc) && (j > 0 || wait_for(do_full, un & 1, wc)) &&
+        ok = wait_for(&v_ready[t % 2], (t / 2) & 1, wc) && (j > 0 || wait_for(do_full, un & 1, wc)) &&
              (t == 0 || wait_for(dp_free, (t - 1) & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          issue_nt<DH>(tD, do_lo, v_lo);
+          issue_nt<DH>(tD, do_lo, v_lo + (t % 2) * (P::T >> 4));
           umma_commit(d_full);
-          umma_commit(v_empty);
+          umma_commit(&v_empty[t % 2]);
           if (!more) umma_commit(do_empty);
         }
       }
@@ -326,13 +338,13 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
         }
       const uint32_t t1 = have ? t + 1 : 0, un1 = more ? un : have ? un + 1 : 0;
       if (next) {
-        ok = wait_for(&k_ready[t1 % 3], (t1 / 3) & 1, wc) && (more || wait_for(&q_full[un1 & 1], (un1 >> 1) & 1, wc));
+        ok = wait_for(&k_ready[t1 % 3], (t1 / 3) & 1, wc) && (more || wait_for(q_full, un1 & 1, wc));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          issue_nt<DH>(tS(t1), q_lo + (un1 & 1) * (P::T >> 4), k_lo + (t1 % 3) * (P::T >> 4));
+          issue_nt<DH>(tS(t1), q_lo, k_lo + (t1 % 3) * (P::T >> 4));
           umma_commit(&s_full[t1 & 1]);
-          if (more ? j + 2 == n : nu.k1 - nu.k0 <= kTile) umma_commit(&q_empty[un1 & 1]);  // the unit's last S
+          if (more ? j + 2 == n : nu.k1 - nu.k0 <= kTile) umma_commit(q_empty);  // the unit's last S
         }
       }
       if (!have && !next) break;
@@ -437,7 +449,6 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
     // ---------------------------------------------------------------- D a unit ahead, and the results
     const int sub = warp & 3, row = sub * 32 + lane;
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
-    constexpr int LPR = DH / 8, RPW = 32 / LPR;
     uint32_t un = 0, on = 0;
     XUnit pu{};
     bool pending = false, ok = true;
@@ -463,35 +474,33 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       if (keys) {
         float* out = vec + (un & 1) * 2 * kTile;
         const int tok = u.q0 + (row >> xg.log2r), h = (u.g << xg.log2r) + (row & (xg.r - 1));
-        out[row] = tok < u.q1 ? -a.lse[(int64_t)h * a.N + tok] * kLog2e : -INFINITY;
-        out[kTile + row] = 0.0f;
-        __syncwarp();
-        if (!(flag & 2)) {
-          const int l = lane % LPR;
-#pragma unroll 4
-          for (int i = 0; i < 32; i += RPW) {
-            const int r = sub * 32 + i + lane / LPR;
-            const int tk = u.q0 + (r >> xg.log2r), hh = (u.g << xg.log2r) + (r & (xg.r - 1));
-            float s = 0.0f;
-            if (tk < u.q1) {
-              const int64_t o = ((int64_t)tk * a.H + hh) * DH + l * 8;
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + o));
-              const uint4 y = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + o));
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+        const bool live = tok < u.q1;
+        const float lse = live ? a.lse[(int64_t)h * a.N + tok] : INFINITY;
+        float D = 0.0f;
+        if (live && !(flag & 2)) {
+          // A thread sums its own row, in whole sectors: rows shared by lanes
+          // took more code, which this warp alone runs, once a unit.
+          const int64_t o = ((int64_t)tok * a.H + h) * DH;
+          const __nv_bfloat16 *px = static_cast<const __nv_bfloat16*>(a.dout) + o,
+                              *py = static_cast<const __nv_bfloat16*>(a.out) + o;
+#pragma unroll 1
+          for (int c = 0; c < DH; c += 64) {
+            uint32_t x[32], y[32];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-                s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
-              }
+            for (int i = 0; i < 4; ++i) {
+              load32(x + 8 * i, px + c + 16 * i);
+              load32(y + 8 * i, py + c + 16 * i);
             }
 #pragma unroll
-            for (int k = LPR / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-            if (l == 0) {
-              out[kTile + r] = s;
-              if (u.split == 0 && tk < u.q1) a.dsum[(int64_t)hh * a.N + tk] = s;
+            for (int i = 0; i < 32; ++i) {
+              D = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), D);
+              D = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), D);
             }
           }
+          if (u.split == 0) a.dsum[(int64_t)h * a.N + tok] = D;
         }
+        out[row] = -lse * kLog2e;
+        out[kTile + row] = D;
         mbar_arrive(&vec_full[un & 1]);
         ++un;
       }
@@ -831,23 +840,23 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
   }
 }
 
-// out = the sum of the shares' rows, for rows of a segment: `keys` rows are
-// [L, H_kv] and part holds two tensors per share, others [N, H] and one.
+// The sum of the shares' rows, for rows of a segment: of dQ ([N, H], one
+// tensor a share), or of dV and dK ([L, H_kv], two; blockIdx.y picks one).
+// Eight threads share a row's piece, each every eighth share, in a fixed order.
 template <int DH>
 __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossArgs a, bool keys, int splits,
-                                                        const float* __restrict__ part, int64_t step,
-                                                        __nv_bfloat16* __restrict__ out) {
+                                                        const float* __restrict__ part) {
+  __shared__ float4 lane_sum[8][32][2];
   if (!segments_ok(a, nullptr)) return;
   const int heads = keys ? a.Hkv : a.H;
-  const int64_t rows = (keys ? a.L : a.N) * heads;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * (DH / 8)) return;
+  const int64_t pieces = (keys ? a.L : a.N) * heads * (DH / 8);
+  const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x;
   const int64_t row = i / (DH / 8) / heads;
-  bool inside = true;
+  bool inside = i < pieces;
   if (!keys) {
-    if (a.q_off) inside = row >= a.q_off[0] && row < a.q_off[a.S];
-  } else if (a.kv_off || a.kv_len) {
-    int lo = 0, hi = a.S - 1;  // the last segment that starts at or before the row and is not empty before it
+    if (a.q_off) inside = inside && row >= a.q_off[0] && row < a.q_off[a.S];
+  } else if (inside && (a.kv_off || a.kv_len)) {
+    int lo = 0, hi = a.S - 1;  // the last segment that starts at or before the row
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (segment(a, mid).k0 <= row) lo = mid; else hi = mid - 1;
@@ -855,27 +864,52 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossArgs a, bool 
     const Seg s = segment(a, lo);
     inside = row >= s.k0 && row < s.k1;
   }
-  if (!inside) return;
-  float v[8] = {};
-#pragma unroll 2
-  for (int s = 0; s < splits; ++s) {
-    const float4* p = reinterpret_cast<const float4*>(part + s * step + i * 8);
-    const float4 x = p[0], y = p[1];
-    v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-    v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+  const int64_t step = pieces * 8 * (keys ? 2 : 1);
+  const float* p = part + (int64_t)blockIdx.y * pieces * 8 + i * 8;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+  if (inside) {
+#pragma unroll 4
+    for (int s = threadIdx.y; s < splits; s += 8) {
+      const float4 u = *reinterpret_cast<const float4*>(p + s * step), v = *reinterpret_cast<const float4*>(p + s * step + 4);
+      x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
   }
-  reinterpret_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  lane_sum[threadIdx.y][threadIdx.x][0] = x;
+  lane_sum[threadIdx.y][threadIdx.x][1] = y;
+  __syncthreads();
+  if (threadIdx.y != 0 || !inside) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    const float4 u = lane_sum[k][threadIdx.x][0], v = lane_sum[k][threadIdx.x][1];
+    x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
+    y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+  }
+  void* out = !keys ? a.dq : blockIdx.y ? a.dk : a.dv;
+  static_cast<uint4*>(out)[i] = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y),
+                                           pack_bf16x2(y.z, y.w));
 }
 
-// Shares of the keys for dQ, as in the forward, and of the queries for dK and
-// dV: four rounds of units on every SM, so that the last one's ragged end
-// costs little.
+// Shares of the keys for dQ, as in the forward.
 int dq_splits(int64_t N, int64_t L, int H, int r, int S) {
   return shares(places_most(N, kTile / r, S) * (H / r), ceil_div(L, S), kTile, kSplitSms);
 }
+// Shares of the queries for dK and dV.  One segment makes equal units: of one
+// to four rounds over the SMs the first that leaves under a twentieth of them
+// idle, else the fullest (48 units: 3 shares, 144 of 148 SMs).  Ragged
+// segments take four rounds, so that the last one's ragged end costs little.
 int dkv_splits(int64_t N, int64_t L, int H_kv, int r, int S) {
-  return shares(places_most(L, kTile, S) * H_kv, ceil_div(N, S), kTile / r, 4 * kSplitSms);
+  const int64_t units = places_most(L, kTile, S) * H_kv;
+  int64_t rounds = 4;
+  if (S == 1 && units > 0) {
+    double best = 0.0;
+    for (int64_t k = 1; k <= 4 && best < 0.95; ++k) {
+      const int64_t sms = k * kSplitSms, n = sms / units;
+      const double used = (double)(n * units) / (double)sms;
+      if (used > best + 1e-9) best = used, rounds = k;
+    }
+  }
+  return shares(units, ceil_div(N, S), kTile / r, rounds * kSplitSms);
 }
 
 struct BwdWs {
@@ -903,19 +937,20 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
             view_2d(&m.v, &m.vv, a.v, a.v_sn, a.v_sh, a.L, a.Hkv, DH);
   if (r > 1)
     ok = ok && make_tmap_heads(&m.q, a.q, DH, a.H, a.N, a.q_sh, a.q_sn, r, base.tokens) &&
-         make_tmap_heads(&m.dout, a.dout, DH, a.H, a.N, DH, HD, r, base.tokens);
+         make_tmap_heads(&m.dout, a.dout, DH, a.H, a.N, DH, HD, r, base.tokens) &&
+         make_tmap_heads(&m.out, a.out, DH, a.H, a.N, DH, HD, r, base.tokens);
   else
     ok = ok && view_2d(&m.q, &m.qv, a.q, a.q_sn, a.q_sh, a.N, a.H, DH) &&
-         view_2d(&m.dout, &m.dv, a.dout, HD, DH, a.N, a.H, DH);
+         view_2d(&m.dout, &m.dv, a.dout, HD, DH, a.N, a.H, DH) &&
+         view_2d(&m.out, &m.dv, a.out, HD, DH, a.N, a.H, DH);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(cross_dq_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess ||
       (e = cudaFuncSetAttribute(cross_dkv_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess)
     return e;
-  auto sum = [&](bool keys, int splits, const float* part, int64_t step, void* out) {
+  auto sum = [&](bool keys, int splits, const float* part) {
     const int64_t n = (keys ? a.L * a.Hkv : a.N * a.H) * (DH / 8);
-    cross_sum_kernel<DH><<<(unsigned)ceil_div(n, 256), 256, 0, c.stream>>>(a, keys, splits, part, step,
-                                                                         static_cast<__nv_bfloat16*>(out));
+    cross_sum_kernel<DH><<<dim3((unsigned)ceil_div(n, 32), keys ? 2 : 1), dim3(32, 8), 0, c.stream>>>(a, keys, splits, part);
     ++*launches;
     return cudaGetLastError();
   };
@@ -930,7 +965,7 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
                                                                           (unsigned long long)c.wait_ns);
     ++*launches;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (part && (e = sum(false, x.splits, part, a.N * HD, a.dq)) != cudaSuccess) return e;
+    if (part && (e = sum(false, x.splits, part)) != cudaSuccess) return e;
   }
   if (a.L > 0) {
     XGrid x = base;
@@ -943,10 +978,7 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
                                                                            (unsigned long long)c.wait_ns);
     ++*launches;
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t kd = a.L * a.Hkv * DH;
-    if (part && ((e = sum(true, x.splits, part, 2 * kd, a.dv)) != cudaSuccess ||
-                 (e = sum(true, x.splits, part + kd, 2 * kd, a.dk)) != cudaSuccess))
-      return e;
+    if (part && (e = sum(true, x.splits, part)) != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
