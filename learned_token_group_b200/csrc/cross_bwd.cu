@@ -597,6 +597,12 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
             if (!wait_for(&y1_empty[s1], ((t1 / 3) & 1) ^ 1, wc)) { ok = false; break; }
             load_tile<DH>(&m.q, m.qv, &y1_full[s1], smem + P::kY1 + s1 * P::T, xg.r, h, tok, keep);
             ++t1;
+            // A tile comes in when the products of the tile before last are
+            // done, and is needed some 2,000 cycles later: from L2 it is there.
+            if (tok + 3 * xg.tokens < u.q1) {
+              prefetch_tile<DH>(&m.q, m.qv, xg.r, h, tok + 3 * xg.tokens);
+              prefetch_tile<DH>(&m.dout, m.dv, xg.r, h, tok + 3 * xg.tokens);
+            }
             if (!wait_for(&y2_empty[s2], ((t2 / 2) & 1) ^ 1, wc)) { ok = false; break; }
             load_tile<DH>(&m.dout, m.dv, &y2_full[s2], smem + P::kY2 + s2 * P::T, xg.r, h, tok, keep);
             ++t2;
@@ -648,20 +654,24 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
       if (!__shfl_sync(0xffffffffu, w, 0)) break;
       const int q0 = __shfl_sync(0xffffffffu, u.q0, 0), q1 = __shfl_sync(0xffffffffu, u.q1, 0),
                 g = __shfl_sync(0xffffffffu, u.g, 0);
+      float lv[4], dv[4];
+      auto fetch = [&](int loop, int tok) {
+        const int rows = min(q1 - tok, xg.tokens) << xg.log2r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = lane + 32 * i;
+          const int64_t at = (int64_t)(head_of(g, loop) + (r & (xg.r - 1))) * a.N + tok + (r >> xg.log2r);
+          lv[i] = r < rows ? -a.lse[at] * kLog2e : -INFINITY;
+          dv[i] = r < rows ? a.dsum[at] : 0.0f;
+        }
+      };
 #pragma unroll 1
       for (int loop = 0; loop < loops && ok; ++loop) {
 #pragma unroll 1
         for (int tok0 = q0; tok0 < q1; tok0 += xg.tokens, ++t) {
           const uint32_t s1 = t % 3, s2 = t % 2;
           const int valid = min(q1 - tok0, xg.tokens) << xg.log2r;
-          float lv[4], dv[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = lane + 32 * i;
-            const int64_t at = (int64_t)(head_of(g, loop) + (r & (xg.r - 1))) * a.N + tok0 + (r >> xg.log2r);
-            lv[i] = r < valid ? -a.lse[at] * kLog2e : -INFINITY;
-            dv[i] = r < valid ? a.dsum[at] : 0.0f;
-          }
+          if (tok0 == q0) fetch(loop, tok0);
           if (lane == 0) w = wait_for(&y1_full[s1], (t / 3) & 1, wc);
           if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
           __syncwarp();
@@ -669,15 +679,18 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
 #pragma unroll
           for (int i = 0; i < 4; ++i) vec1[s1 * kTile + lane + 32 * i] = lv[i];
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&y1_ready[s1]);
-            w = wait_for(&y2_full[s2], (t / 2) & 1, wc);
-          }
+          float nv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) nv[i] = dv[i];
+          if (lane == 0) mbar_arrive(&y1_ready[s1]);
+          // the next tile's, before the wait for this one's dO
+          if (tok0 + xg.tokens < q1) fetch(loop, tok0 + xg.tokens);
+          if (lane == 0) w = wait_for(&y2_full[s2], (t / 2) & 1, wc);
           if (!__shfl_sync(0xffffffffu, w, 0)) { ok = false; break; }
           __syncwarp();
           zero_rows<DH>(smem + P::kY2 + s2 * P::T, valid, lane);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vec2[s2 * kTile + lane + 32 * i] = dv[i];
+          for (int i = 0; i < 4; ++i) vec2[s2 * kTile + lane + 32 * i] = nv[i];
           __syncwarp();
           if (lane == 0) mbar_arrive(&y2_ready[s2]);
         }
