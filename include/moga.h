@@ -434,7 +434,7 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
  * Out: out bf16 [N, H, d_h], dense; lse fp32 [H, N] or NULL: the natural
  *      log-sum-exp of each query's scaled scores.  A query whose segment has
  *      no keys gets out = 0 and lse = -inf.  Rows of no segment are left as
- *      they were.  Values of rows that no segment reads (padding) have no
+ *      they were (fill = 0) or set likewise (fill = 1).  Values of rows that no segment reads (padding) have no
  *      effect, infinities and NaN included.
  * Limits: d_h 64 or 128; N, L < 2^30; N * H, L * H_kv < 2^31; H a multiple
  * of H_kv; S <= 1024.
@@ -443,15 +443,16 @@ size_t moga_cross_attn_workspace_size(int64_t N, int64_t L, int H, int H_kv, int
 moga_status moga_cross_attn(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k, int64_t k_stride_n,
                             int64_t k_stride_h, const void* v, int64_t v_stride_n, int64_t v_stride_h, int64_t N,
                             int64_t L, int H, int H_kv, int d_h, const int32_t* q_offsets, const int32_t* kv_offsets,
-                            const int32_t* kv_lens, int S, void* out, float* lse, void* ws, size_t ws_bytes,
-                            void* stream);
+                            const int32_t* kv_lens, int S, void* out, float* lse, int fill, void* ws,
+                            size_t ws_bytes, void* stream);
 
 /* moga_cross_attn_backward: gradients of moga_cross_attn from dout (bf16
  * [N, H, d_h], dense), the forward's inputs and its out and lse.
  * Out: dq bf16 [N, H, d_h], dk, dv bf16 [L, H_kv, d_h], dense; dk and dv are
- *      summed over the query heads that share a key head.  Rows of no segment
- *      (and key rows past a segment's length) are left as they were.  All sums
- *      are taken in a fixed order.
+ *      summed over the query heads that share a key head.  Query rows of no
+ *      segment are left as they were (fill = 0) or get dq = 0 (fill = 1); key
+ *      rows of no segment, or past its length, are left as they were.  All
+ *      sums are taken in a fixed order.
  * dout, out, dq, dk, dv and ws are 32-byte aligned (whole sectors are read and
  * written).
  * Workspace: moga_cross_attn_backward_workspace_size(...) bytes. */
@@ -461,7 +462,7 @@ moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_
                                      int64_t v_stride_n, int64_t v_stride_h, int64_t N, int64_t L, int H, int H_kv,
                                      int d_h, const int32_t* q_offsets, const int32_t* kv_offsets,
                                      const int32_t* kv_lens, int S, const void* out, const float* lse, void* dq,
-                                     void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
+                                     void* dk, void* dv, int fill, void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- host pipeline
  * A pipeline runs the visual block of moga_layer_ex (same arithmetic, same

@@ -12,6 +12,7 @@ Eq. 5, Algorithm 1, STGA).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional, Sequence
@@ -108,10 +109,10 @@ def get_lib():
                                             _P, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
         "moga_cross_attn_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
         "moga_cross_attn": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P,
-                                 _I, _P, _P, _P, _SZ, _P]),
+                                 _I, _P, _P, _I, _P, _SZ, _P]),
         "moga_cross_attn_backward_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
         "moga_cross_attn_backward": (_I, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I,
-                                          _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+                                          _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -522,15 +523,20 @@ class MogaFunction(torch.autograd.Function):
 
 
 # ----------------------------------------------------------------------------- queries and keys, cross attention
-def _on(dev: torch.device, **tensors):
-    """Every given tensor must be on the CUDA device ``dev``."""
-    for n, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{n} must be on {dev}, got {t.device}")
+# A small call is bound by the host, so the checks below cost tenths of a
+# microsecond each: attributes are read once, and messages made on failure.
+_BF16 = (torch.bfloat16,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(dev).cuda_stream without its objects
 
 
-def _rows(t: torch.Tensor, name: str, dtypes):
-    """A [tokens, heads, d_h] tensor or view whose heads are dense: its shape and its two strides."""
+@functools.lru_cache(maxsize=256)
+def _triple(a: int, b: int, c: int):
+    return (ctypes.c_int * 3)(a, b, c)
+
+
+def _heads(t: torch.Tensor, name: str, dtypes):
+    """Refuses what is not a [tokens, heads, d_h] CUDA tensor or view of one of the types with dense heads."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 3:
@@ -539,7 +545,11 @@ def _rows(t: torch.Tensor, name: str, dtypes):
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.stride(2) != 1:
         raise ValueError(f"{name}'s heads must be dense")
-    return t.shape, t.stride()
+
+
+def _device(t: Optional[torch.Tensor], name: str, dev: torch.device):
+    if t is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
 def _readable(t: Optional[torch.Tensor], head_major: bool = False):
@@ -555,8 +565,9 @@ def _readable(t: Optional[torch.Tensor], head_major: bool = False):
 
 
 def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
-    _on(dev, **{name: t})
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
     return t
@@ -564,18 +575,23 @@ def _dense(t: torch.Tensor, name: str, shape, dtype, dev):
 
 def _call(dev: torch.device, what: str, *args):
     """Calls the library on ``dev`` and its current stream (the last argument)."""
-    fn = getattr(get_lib(), what)
+    fn = getattr(_lib or get_lib(), what)
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(dev.index))
     if st != 0:
         raise MogaError(st, what)
 
 
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _like(x: torch.Tensor, dtype=None):
+    """A dense tensor of x's shape."""
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def rope_table(P: int, d_h: int, axes: Sequence[int], theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -587,48 +603,54 @@ def rope_table(P: int, d_h: int, axes: Sequence[int], theta: float = 10000.0, de
     if P < 1 or d_h not in (64, 128):
         raise ValueError(f"a table needs P >= 1 positions and d_h 64 or 128, got {P} and {d_h}")
     table = torch.empty((P, d_h // 2, 2), dtype=torch.float32, device=dev)
-    _call(dev, "moga_rope_table", P, d_h, _int3(axes), float(theta), _at(table))
+    _call(dev, "moga_rope_table", P, d_h, _triple(*map(int, axes)), float(theta), table.data_ptr())
     return table
 
 
 def _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves):
-    """Checks the shared arguments: (device, N, heads, d_h, the C call's arguments from q on)."""
-    x = q if q is not None else k
+    """Checks the shared arguments: (device, d_h, the C call's arguments from q on)."""
+    x = k if q is None else q
     if x is None:
         raise ValueError("one of q and k must be given")
-    (N, _, d_h), _ = _rows(x, "q" if q is not None else "k", (torch.bfloat16, torch.float32))
-    dev, args, heads = x.device, [], []
-    for n, t in (("q", q), ("k", k)):
-        if t is None:
-            args += [None, 0, 0]
-            heads.append(0)
-            continue
-        shape, st = _rows(t, n, (x.dtype,))
-        if shape[0] != N or shape[2] != d_h:
-            raise ValueError(f"q and k must have the same tokens and d_h, got {tuple(x.shape)} and {tuple(shape)}")
-        _on(dev, **{n: t})
-        args += [t.data_ptr(), st[0], st[1]]
-        heads.append(shape[1])
-    for n, w in (("w_q", w_q), ("w_k", w_k)):
-        if w is not None:
-            _dense(w, n, (d_h,), torch.float32, dev)
-    P, axes3, grid3 = 0, None, None
+    _heads(x, "k" if q is None else "q", _BF16_F32)
+    dev, dtype = x.device, x.dtype
+    N, H, d_h = x.shape
+    sn, sh, _ = x.stride()
+    if q is None:
+        args = [None, 0, 0, x.data_ptr(), sn, sh, MOGA_BF16 if dtype is torch.bfloat16 else MOGA_F32, N, 0, H, d_h]
+    else:
+        args = [x.data_ptr(), sn, sh, None, 0, 0, MOGA_BF16 if dtype is torch.bfloat16 else MOGA_F32, N, H, 0, d_h]
+        if k is not None:
+            _heads(k, "k", (dtype,))
+            n, args[9], d = k.shape
+            if n != N or d != d_h:
+                raise ValueError(f"q and k must have the same tokens and d_h, got {tuple(x.shape)} and "
+                                 f"{tuple(k.shape)}")
+            _device(k, "k", dev)
+            args[3] = k.data_ptr()
+            args[4], args[5], _ = k.stride()
+    if w_q is not None:
+        _dense(w_q, "w_q", (d_h,), torch.float32, dev)
+    if w_k is not None:
+        _dense(w_k, "w_k", (d_h,), torch.float32, dev)
+    P = 0
     if table is not None:
         if table.dim() != 3 or axes is None:
             raise ValueError("a table is [P, d_h / 2, 2] and needs axes")
-        P, axes3 = table.shape[0], _int3(axes)
+        P = table.shape[0]
         _dense(table, "table", (P, d_h // 2, 2), torch.float32, dev)
         if (grid is None) == (positions is None):
             raise ValueError("a table needs a grid or positions, one of them")
-        grid3 = None if grid is None else _int3(grid)
+        axes = _triple(*map(int, axes))
+        grid = None if grid is None else _triple(*map(int, grid))
     elif grid is not None or positions is not None:
         raise ValueError("grid and positions need a table")
+    else:
+        axes = None
     if positions is not None:
         _dense(positions, "positions", (N, 3), torch.int32, dev)
-    dt = MOGA_BF16 if x.dtype == torch.bfloat16 else MOGA_F32
-    args += [dt, N, heads[0], heads[1], d_h, _at(w_q), _at(w_k), float(eps), _at(table), P, axes3, grid3,
-             int(token0), _at(positions), int(bool(halves))]
-    return dev, N, heads, d_h, args
+    args += (_at(w_q), _at(w_k), eps, _at(table), P, axes, grid, token0, _at(positions), 1 if halves else 0)
+    return dev, d_h, args
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], w_q: Optional[torch.Tensor] = None,
@@ -645,18 +667,18 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], w_q: Opti
     (q_out, k_out), bf16 and dense, None for a side that was None; out: such a
     pair to write to.  ws (``workspace``): for positions outside the table,
     which ``sync_status`` reports; it is made when positions are given without it."""
-    dev, N, heads, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
-    outs = [None, None]
-    for i, n in enumerate(("q_out", "k_out")):
-        if heads[i]:
-            shape = (N, heads[i], d_h)
-            outs[i] = (torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None
-                       else _dense(out[i], n, shape, torch.bfloat16, dev))
+    dev, _, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+    if out is None:
+        q_out = None if q is None else _like(q, torch.bfloat16)
+        k_out = None if k is None else _like(k, torch.bfloat16)
+    else:
+        q_out = None if q is None else _dense(out[0], "q_out", q.shape, torch.bfloat16, dev)
+        k_out = None if k is None else _dense(out[1], "k_out", k.shape, torch.bfloat16, dev)
     if ws is None and positions is not None:
         ws = workspace(256, dev)
-    _on(dev, ws=ws)
-    _call(dev, "moga_qk_norm_rope", *args, _at(outs[0]), _at(outs[1]), _at(ws), 0 if ws is None else ws.numel())
-    return outs[0], outs[1]
+    _device(ws, "ws", dev)
+    _call(dev, "moga_qk_norm_rope", *args, _at(q_out), _at(k_out), _at(ws), 0 if ws is None else ws.numel())
+    return q_out, k_out
 
 
 def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
@@ -669,23 +691,24 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     dict(dq, dk, dw_q, dw_k, ws) from the gradients of its outputs (bf16,
     dense).  dq and dk have the inputs' type; dw_q, dw_k are fp32 [d_h], None
     for a weight that is None.  Pass the ws back to reuse it."""
-    dev, N, heads, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+    dev, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
     g = {"dq": None, "dk": None, "dw_q": None, "dw_k": None}
-    for i, (n, d, x, w) in enumerate((("q", dq_out, q, w_q), ("k", dk_out, k, w_k))):
-        if not heads[i]:
+    for n, d, x, w in (("q", dq_out, q, w_q), ("k", dk_out, k, w_k)):
+        if x is None:
             continue
         if d is None:
             raise ValueError(f"d{n}_out is missing")
-        _dense(d, f"d{n}_out", (N, heads[i], d_h), torch.bfloat16, dev)
-        g[f"d{n}"] = torch.empty((N, heads[i], d_h), dtype=x.dtype, device=dev)
+        _dense(d, f"d{n}_out", x.shape, torch.bfloat16, dev)
+        g["d" + n] = _like(x)
         if w is not None:
-            g[f"dw_{n}"] = torch.empty(d_h, dtype=torch.float32, device=dev)
+            g["dw_" + n] = torch.empty_like(w)
     need = get_lib().moga_qk_norm_rope_backward_workspace_size(d_h)
     if ws is None or ws.numel() < need:
         ws = workspace(need, dev)
-    _on(dev, ws=ws)
-    _call(dev, "moga_qk_norm_rope_backward", _at(dq_out) if heads[0] else None, _at(dk_out) if heads[1] else None,
-          *args, _at(g["dq"]), _at(g["dk"]), _at(g["dw_q"]), _at(g["dw_k"]), _at(ws), ws.numel())
+    _device(ws, "ws", dev)
+    _call(dev, "moga_qk_norm_rope_backward", None if q is None else dq_out.data_ptr(),
+          None if k is None else dk_out.data_ptr(), *args, _at(g["dq"]), _at(g["dk"]), _at(g["dw_q"]), _at(g["dw_k"]),
+          ws.data_ptr(), ws.numel())
     g["ws"] = ws
     return g
 
@@ -717,30 +740,37 @@ class QkNormRopeFunction(torch.autograd.Function):
 
 
 def _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens):
-    """Checks the shared arguments: (device, N, L, H, H_kv, d_h, S, the C call's arguments from q on)."""
-    (N, H, d_h), qs = _rows(q, "q", (torch.bfloat16,))
-    (L, Hk, dk), ks = _rows(k, "k", (torch.bfloat16,))
-    sv, vs = _rows(v, "v", (torch.bfloat16,))
-    if dk != d_h or tuple(sv) != (L, Hk, dk) or Hk == 0 or H % Hk:
-        raise ValueError(f"k and v must be [L, H_kv, {d_h}] with H_kv dividing {H}, got {tuple(k.shape)} and {tuple(sv)}")
+    """Checks the shared arguments: (device, (N, L, H, H_kv, d_h, S), the C call's arguments from q on)."""
+    _heads(q, "q", _BF16)
+    _heads(k, "k", _BF16)
+    _heads(v, "v", _BF16)
     dev = q.device
-    _on(dev, k=k, v=v)
-    if (q_offsets is None) != (kv_offsets is None) and (q_offsets if kv_offsets is None else kv_offsets).numel() != 2:
-        raise ValueError("several segments need q_offsets and kv_offsets")
+    N, H, d_h = q.shape
+    L, Hk, d = k.shape
+    if d != d_h or v.shape != k.shape or Hk == 0 or H % Hk:
+        raise ValueError(f"k and v must be [L, H_kv, {d_h}] with H_kv dividing {H}, got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    _device(k, "k", dev)
+    _device(v, "v", dev)
     S = 1
-    for n, t in (("q_offsets", q_offsets), ("kv_offsets", kv_offsets)):
-        if t is not None:
-            if t.dim() != 1 or t.numel() < 2:
-                raise ValueError(f"{n} must be int32 [S + 1]")
-            S = t.numel() - 1
-    for n, t, m in (("q_offsets", q_offsets, S + 1), ("kv_offsets", kv_offsets, S + 1), ("kv_lens", kv_lens, S)):
-        if t is not None:
-            _dense(t, n, (m,), torch.int32, dev)
-    # the stride of a dimension of one element says nothing
-    st = lambda t, s: (s[0] if t.shape[0] > 1 else t.shape[1] * d_h, s[1] if t.shape[1] > 1 else d_h)  # noqa: E731
-    args = [q.data_ptr(), *st(q, qs), k.data_ptr(), *st(k, ks), v.data_ptr(), *st(v, vs), N, L, H, Hk, d_h,
-            _at(q_offsets), _at(kv_offsets), _at(kv_lens), S]
-    return dev, N, L, H, Hk, d_h, S, args
+    if q_offsets is not None or kv_offsets is not None or kv_lens is not None:
+        for n, t in (("q_offsets", q_offsets), ("kv_offsets", kv_offsets)):
+            if t is not None:
+                if t.dim() != 1 or t.numel() < 2:
+                    raise ValueError(f"{n} must be int32 [S + 1]")
+                S = max(S, t.numel() - 1)
+        if S > 1 and (q_offsets is None or kv_offsets is None):
+            raise ValueError("several segments need q_offsets and kv_offsets")
+        for n, t, m in (("q_offsets", q_offsets, S + 1), ("kv_offsets", kv_offsets, S + 1), ("kv_lens", kv_lens, S)):
+            if t is not None:
+                _dense(t, n, (m,), torch.int32, dev)
+    sizes = (N, L, H, Hk, d_h, S)
+    args = []
+    for t, n, h in ((q, N, H), (k, L, Hk), (v, L, Hk)):
+        sn, sh, _ = t.stride()  # the stride of a dimension of one element says nothing
+        args += (t.data_ptr(), sn if n > 1 else h * d_h, sh if h > 1 else d_h)
+    args += (N, L, H, Hk, d_h, _at(q_offsets), _at(kv_offsets), _at(kv_lens), S)
+    return dev, sizes, args
 
 
 def cross_attn_workspace_size(q: torch.Tensor, k: torch.Tensor, segments: int = 1, backward: bool = False) -> int:
@@ -760,22 +790,19 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opt
     kv_lens[s] of them (by default up to the next offset); device int32.
     Without offsets all queries attend to all keys.  Returns out [N, H, d_h],
     or (out, lse [H, N]) with return_lse.  Rows of no segment are zero (lse
-    -inf) in an output made here, and left as they were in a given ``out``."""
-    dev, N, L, H, Hk, d_h, S, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
-    if out is None:
-        make = torch.empty if q_offsets is None else torch.zeros
-        out = make((N, H, d_h), dtype=torch.bfloat16, device=dev)
+    -inf) in an output made here, and left as they were (lse not written) in
+    a given ``out``."""
+    dev, sizes, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
+    fill = out is None
+    if fill:
+        out = _like(q)
     else:
-        _dense(out, "out", (N, H, d_h), torch.bfloat16, dev)
-    lse = None
-    if return_lse:
-        lse = (torch.empty((H, N), dtype=torch.float32, device=dev) if q_offsets is None
-               else torch.full((H, N), float("-inf"), dtype=torch.float32, device=dev))
-    need = get_lib().moga_cross_attn_workspace_size(N, L, H, Hk, d_h, S)
+        _dense(out, "out", q.shape, torch.bfloat16, dev)
+    lse = torch.empty((sizes[2], sizes[0]), dtype=torch.float32, device=dev) if return_lse else None
     if ws is None:
-        ws = workspace(need, dev)
-    _on(dev, ws=ws)
-    _call(dev, "moga_cross_attn", *args, out.data_ptr(), _at(lse), ws.data_ptr(), ws.numel())
+        ws = workspace(get_lib().moga_cross_attn_workspace_size(*sizes), dev)
+    _device(ws, "ws", dev)
+    _call(dev, "moga_cross_attn", *args, out.data_ptr(), _at(lse), int(fill), ws.data_ptr(), ws.numel())
     return (out, lse) if return_lse else out
 
 
@@ -786,20 +813,19 @@ def cross_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
     """Gradients of ``cross_attn`` (moga_cross_attn_backward in moga.h): dict(dq,
     dk, dv, ws), bf16 and dense, from dout and the forward's out and lse.  Rows
     of no segment get zero.  Pass the ws back to reuse it."""
-    dev, N, L, H, Hk, d_h, S, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
-    _dense(dout, "dout", (N, H, d_h), torch.bfloat16, dev)
-    _dense(out, "out", (N, H, d_h), torch.bfloat16, dev)
-    _dense(lse, "lse", (H, N), torch.float32, dev)
-    make_q = torch.empty if q_offsets is None else torch.zeros
-    make_k = torch.empty if kv_offsets is None and kv_lens is None else torch.zeros
-    dq = make_q((N, H, d_h), dtype=torch.bfloat16, device=dev)
-    dk, dv = (make_k((L, Hk, d_h), dtype=torch.bfloat16, device=dev) for _ in range(2))
-    need = get_lib().moga_cross_attn_backward_workspace_size(N, L, H, Hk, d_h, S)
+    dev, sizes, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
+    _dense(dout, "dout", q.shape, torch.bfloat16, dev)
+    _dense(out, "out", q.shape, torch.bfloat16, dev)
+    _dense(lse, "lse", (sizes[2], sizes[0]), torch.float32, dev)
+    dq = _like(q)
+    make = torch.empty if kv_offsets is None and kv_lens is None else torch.zeros  # keys may have gaps
+    dk, dv = make((2, *k.shape), dtype=torch.bfloat16, device=dev)
+    need = get_lib().moga_cross_attn_backward_workspace_size(*sizes)
     if ws is None or ws.numel() < need:
         ws = workspace(need, dev)
-    _on(dev, ws=ws)
+    _device(ws, "ws", dev)
     _call(dev, "moga_cross_attn_backward", dout.data_ptr(), *args, out.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-          dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel())
+          dk.data_ptr(), dv.data_ptr(), 1, ws.data_ptr(), ws.numel())
     return {"dq": dq, "dk": dk, "dv": dv, "ws": ws}
 
 

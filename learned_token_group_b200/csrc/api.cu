@@ -1281,17 +1281,19 @@ size_t moga_cross_attn_workspace_size(int64_t N, int64_t L, int H, int H_kv, int
 moga_status moga_cross_attn(const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh,
                             const void* v, int64_t v_sn, int64_t v_sh, int64_t N, int64_t L, int H, int H_kv, int d_h,
                             const int32_t* q_offsets, const int32_t* kv_offsets, const int32_t* kv_lens, int S,
-                            void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+                            void* out, float* lse, int fill, void* ws, size_t ws_bytes, void* stream) {
   CrossArgs a{};
   const moga_status st = cross_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, v, v_sn, v_sh, N, L, H, H_kv, d_h, q_offsets,
                                     kv_offsets, kv_lens, S);
   if (st != MOGA_OK) return st;
-  if ((N > 0 && !out) || !aligned16(out) || !aligned4(lse) || !ws || !aligned16(ws)) return MOGA_ERR_INVALID_ARG;
+  if ((N > 0 && !out) || !aligned16(out) || !aligned4(lse) || fill < 0 || fill > 1 || !ws || !aligned16(ws))
+    return MOGA_ERR_INVALID_ARG;
   if (ws_bytes < moga_cross_attn_workspace_size(N, L, H, H_kv, d_h, S)) return MOGA_ERR_WORKSPACE;
   DevCtx c;
   if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
   a.out = out;
   a.lse = lse;
+  a.fill = fill;
   a.withhold = g_debug_inject.load(std::memory_order_relaxed) == 1;
   int launches = 0;
   const cudaError_t e = launch_cross_attn(c, a, (uint8_t*)ws + kHeader, &launches);
@@ -1308,15 +1310,15 @@ moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_
                                      int64_t k_sn, int64_t k_sh, const void* v, int64_t v_sn, int64_t v_sh, int64_t N,
                                      int64_t L, int H, int H_kv, int d_h, const int32_t* q_offsets,
                                      const int32_t* kv_offsets, const int32_t* kv_lens, int S, const void* out,
-                                     const float* lse, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
-                                     void* stream) {
+                                     const float* lse, void* dq, void* dk, void* dv, int fill, void* ws,
+                                     size_t ws_bytes, void* stream) {
   CrossArgs a{};
   const moga_status st = cross_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, v, v_sn, v_sh, N, L, H, H_kv, d_h, q_offsets,
                                     kv_offsets, kv_lens, S);
   if (st != MOGA_OK) return st;
   if ((N > 0 && (!dout || !out || !lse || !dq)) || (L > 0 && (!dk || !dv))) return MOGA_ERR_INVALID_ARG;
   if (!aligned32(dout) || !aligned32(out) || !aligned4(lse) || !aligned32(dq) || !aligned32(dk) || !aligned32(dv) ||
-      !ws || !aligned32(ws))
+      fill < 0 || fill > 1 || !ws || !aligned32(ws))
     return MOGA_ERR_INVALID_ARG;
   if (ws_bytes < moga_cross_attn_backward_workspace_size(N, L, H, H_kv, d_h, S)) return MOGA_ERR_WORKSPACE;
   DevCtx c;
@@ -1327,6 +1329,7 @@ moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
+  a.fill = fill;
   int launches = 0;
   const cudaError_t e = launch_cross_bwd(c, a, (uint8_t*)ws + kHeader, &launches);
   count((uint64_t)launches);

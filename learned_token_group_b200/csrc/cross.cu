@@ -571,6 +571,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         }
       }
     }
+    fill_rows<DH>(a, a.out, a.lse, (int64_t)blockIdx.x * 128 + threadIdx.x - 384, (int64_t)gridDim.x * 128);
   }
   tc_fence_before();
   __syncthreads();
@@ -637,7 +638,8 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
     pl = reinterpret_cast<float*>(ws);
     po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 4, 256));
   }
-  cudaError_t e = cudaFuncSetAttribute(cross_fwd_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(cross_fwd_kernel<DH>, P::kBytes, c.device, &allowed);
   if (e != cudaSuccess) return e;
   const int64_t units = places_most(a.N, 2 * x.tokens, a.S) * x.splits * x.heads;
   const unsigned grid = (unsigned)std::min<int64_t>(units, c.num_sms);

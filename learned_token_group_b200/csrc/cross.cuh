@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -264,6 +266,20 @@ struct XView {
   int x, y;
 };
 
+// Query rows of no segment (before the first and behind the last): 0, and
+// lse = -inf where it is given.  One thread of `threads` in the grid.
+template <int DH>
+__device__ __forceinline__ void fill_rows(const CrossArgs& a, void* out, float* lse, int64_t thread, int64_t threads) {
+  if (!a.fill || !a.q_off) return;
+  const int64_t lo = a.q_off[0], hi = a.q_off[a.S], n = lo + a.N - hi;
+  for (int64_t i = thread; i < n * a.H * (DH / 8); i += threads) {
+    const int64_t r = i / (DH / 8) / a.H, tok = r < lo ? r : r - lo + hi;
+    const int64_t rest = i - r * a.H * (DH / 8);
+    static_cast<uint4*>(out)[tok * a.H * (DH / 8) + rest] = make_uint4(0, 0, 0, 0);
+    if (lse && rest % (DH / 8) == 0) lse[rest / (DH / 8) * a.N + tok] = -INFINITY;
+  }
+}
+
 // One operand tile: 128 rows of one head (2-D view), or 128 / r tokens of r heads (3-D).
 template <int DH>
 __device__ __forceinline__ void load_tile(const CUtensorMap* map, const XView& v, uint64_t* bar, uint8_t* dst, int r,
@@ -327,6 +343,16 @@ inline int pack_of(const CrossArgs& a) {
   const int r = a.H / a.Hkv;
   if (a.N == 0 || r < 2 || r > 64 || (r & (r - 1))) return 1;
   return a.q_sn >= (a.H - 1) * a.q_sh + a.d_h && a.q_sn % a.q_sh == 0 ? r : 1;
+}
+
+// The kernel's shared memory, allowed once per device.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, int device, std::atomic<uint64_t>* done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline void set_steps(XGrid* x, int64_t grid) {

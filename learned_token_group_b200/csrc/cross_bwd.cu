@@ -509,6 +509,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       if (keys) pu = u; else write(u, false);
     }
     if (ok && pending) finish();
+    fill_rows<DH>(a, a.dq, nullptr, (int64_t)blockIdx.x * 128 + threadIdx.x - 384, (int64_t)gridDim.x * 128);
   }
   tc_fence_before();
   __syncthreads();
@@ -958,8 +959,9 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
          view_2d(&m.out, &m.dv, a.out, HD, DH, a.N, a.H, DH);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e;
-  if ((e = cudaFuncSetAttribute(cross_dq_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess ||
-      (e = cudaFuncSetAttribute(cross_dkv_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess)
+  static std::atomic<uint64_t> dq_allowed{0}, dkv_allowed{0};
+  if ((e = allow_smem(cross_dq_kernel<DH>, P::kBytes, c.device, &dq_allowed)) != cudaSuccess ||
+      (e = allow_smem(cross_dkv_kernel<DH>, P::kBytes, c.device, &dkv_allowed)) != cudaSuccess)
     return e;
   auto sum = [&](bool keys, int splits, const float* part) {
     const int64_t n = (keys ? a.L * a.Hkv : a.N * a.H) * (DH / 8);

@@ -28,7 +28,10 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kRows = 4;  // rows of one lane group in flight
+// Rows of one lane group in flight: 64 bytes a lane and tensor (six rows cover
+// 12 heads of 128 channels in one item).
+template <typename T>
+constexpr int kRows = sizeof(T) == 2 ? 6 : 3;
 
 template <typename T>
 struct Raw;  // eight channels as loaded
@@ -189,9 +192,9 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_kernel(const NormAr
     const int t = it.chunk >= a.chunks[0];  // 0: query heads, 1: key heads
     const int h0 = (t ? it.chunk - a.chunks[0] : it.chunk) * a.rows[t] * RPW + grp;
     const T* x = static_cast<const T*>(a.x[t]) + it.n * a.sn[t];
-    Raw<T> raw[kRows];
+    Raw<T> raw[kRows<T>];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < kRows<T>; ++u) {
       const int h = h0 + u * RPW;
       raw[u] = Raw<T>{};
       if (u < a.rows[t] && h < a.heads[t]) load8<DH, kHalves>(raw[u], x + h * a.sh[t], l);
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_kernel(const NormAr
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y[t]) + it.n * a.heads[t] * DH;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < kRows<T>; ++u) {
       if (u >= a.rows[t]) break;
       const int h = h0 + u * RPW;
       float v[8];
@@ -235,10 +238,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const No
     const int h0 = (t ? it.chunk - a.chunks[0] : it.chunk) * a.rows[t] * RPW + grp;
     const T* x = static_cast<const T*>(a.x[t]) + it.n * a.sn[t];
     const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(a.dy[t]) + it.n * a.heads[t] * DH;
-    Raw<T> raw[kRows];
-    Raw<__nv_bfloat16> grad[kRows];
+    Raw<T> raw[kRows<T>];
+    Raw<__nv_bfloat16> grad[kRows<T>];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < kRows<T>; ++u) {
       const int h = h0 + u * RPW;
       raw[u] = Raw<T>{};
       grad[u] = Raw<__nv_bfloat16>{};
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const No
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;
     T* dx = static_cast<T*>(a.y[t]) + it.n * a.heads[t] * DH;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < kRows<T>; ++u) {
       if (u >= a.rows[t]) break;
       const int h = h0 + u * RPW;
       float v[8], g[8];
@@ -371,9 +374,9 @@ cudaError_t launch_rope_table(const DevCtx& c, int P, int d_h, const int* axes, 
 cudaError_t launch_norm_rope(const DevCtx& c, NormArgs a, int d_h, bool bf16, bool halves, bool backward,
                              float* dwq, float* dwk, int* launches) {
   // Heads are split evenly over chunks of at most kRows rows per lane group.
-  const int rpw = 256 / d_h;
+  const int rpw = 256 / d_h, most = bf16 ? kRows<__nv_bfloat16> : kRows<float>;
   for (int t = 0; t < 2; ++t) {
-    a.chunks[t] = (int)ceil_div(a.heads[t], (int64_t)rpw * kRows);
+    a.chunks[t] = (int)ceil_div(a.heads[t], (int64_t)rpw * most);
     a.rows[t] = a.chunks[t] ? (int)ceil_div(a.heads[t], (int64_t)rpw * a.chunks[t]) : 0;
   }
   a.half = d_h / 2;

@@ -137,7 +137,7 @@ def test_rope_table_refusals(lib):
 
 
 CROSS = dict(q=P, qs=(512, 128), k=P, ks=(256, 128), v=P, vs=(256, 128), N=100, L=50, H=4, Hk=2, d=128, qo=None, ko=None,
-             kl=None, S=1, out=P, lse=None, ws=P, wsb=BIG)
+             kl=None, S=1, out=P, lse=None, fill=0, ws=P, wsb=BIG)
 CROSS_REFUSALS = [
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(q=P + 8), INVALID),
     (dict(H=0), INVALID), (dict(Hk=0), INVALID), (dict(H=5), INVALID), (dict(N=-1), INVALID), (dict(L=-1), INVALID),
@@ -149,6 +149,7 @@ CROSS_REFUSALS = [
     (dict(qs=(64, 128)), UNSUPPORTED), (dict(qs=(512, 64)), UNSUPPORTED),
     (dict(qs=(128, 12672)), UNSUPPORTED),              # heads overlap: 99 token strides, 100 tokens
     (dict(qs=(256, 12672 + 136)), UNSUPPORTED),        # the head stride is no whole number of token strides
+    (dict(fill=2), INVALID), (dict(fill=-1), INVALID),
     (dict(qs=(448, 128)), UNSUPPORTED),                # a token's heads reach into the next token
 ]
 CROSS_REFUSALS_FWD = CROSS_REFUSALS + [
@@ -160,7 +161,7 @@ CROSS_REFUSALS_FWD = CROSS_REFUSALS + [
 def _cross(lib, **kw):
     a = dict(CROSS, **kw)
     return lib.moga_cross_attn(a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["N"], a["L"], a["H"], a["Hk"],
-                               a["d"], a["qo"], a["ko"], a["kl"], a["S"], a["out"], a["lse"], a["ws"], a["wsb"], None)
+                               a["d"], a["qo"], a["ko"], a["kl"], a["S"], a["out"], a["lse"], a["fill"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("bad,status", CROSS_REFUSALS_FWD, ids=[str(b) for b, _ in CROSS_REFUSALS_FWD])
@@ -172,7 +173,7 @@ def _cross_back(lib, dout=P, dq=P, dk=P, dv=P, **kw):
     a = dict(CROSS, lse=P, **kw)
     return lib.moga_cross_attn_backward(dout, a["q"], *a["qs"], a["k"], *a["ks"], a["v"], *a["vs"], a["N"], a["L"],
                                         a["H"], a["Hk"], a["d"], a["qo"], a["ko"], a["kl"], a["S"], a["out"], a["lse"],
-                                        dq, dk, dv, a["ws"], a["wsb"], None)
+                                        dq, dk, dv, a["fill"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("bad,status", CROSS_REFUSALS, ids=[str(b) for b, _ in CROSS_REFUSALS])
@@ -183,7 +184,7 @@ def test_cross_backward_refusals(lib, bad, status):
 def test_cross_backward_refuses_missing_outputs_and_small_workspaces(lib):
     for n in ("dout", "dq", "dk", "dv", "out"):
         assert _cross_back(lib, **{n: None}) == INVALID
-        assert _cross_back(lib, **{n: P + 8}) == INVALID
+        assert _cross_back(lib, **{n: P + 16}) == INVALID          # 32-byte sectors
     need = lib.moga_cross_attn_backward_workspace_size(100, 50, 4, 2, 128, 1)
     assert _cross_back(lib, wsb=need - 1) == WORKSPACE
     assert lib.moga_cross_attn_workspace_size(-1, 50, 4, 2, 128, 1) == 0
