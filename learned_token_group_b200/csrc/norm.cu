@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* __restrict__
   __shared__ double sum[32][33];
   const int i = blockIdx.x * 32 + threadIdx.x;
   double v = 0.0;
+#pragma unroll 10
   for (int b = threadIdx.y; b < blocks; b += 32) v += part[(int64_t)b * 2 * DH + i];
   sum[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
