@@ -70,7 +70,10 @@ struct XMaps {
   XView qv, kv, vv;
 };
 
-template <int DH>
+// kOne: units with one query tile take turns in both S buffers.  For calls of
+// few rows a segment: 77 queries x 187,200 keys 272 -> 237 us; elsewhere the
+// code it adds costs 4 %.
+template <int DH, bool kOne>
 __global__ void __launch_bounds__(kXThreads, 1)
 cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid xg, float* part_o, float* part_lse,
                  int withhold, int* status, unsigned long long wait_ns) {
@@ -81,22 +84,27 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
   uint64_t* q_full = bars;                     // [2]
   uint64_t* q_empty = bars + 2;                // [2]
-  uint64_t* s_full = bars + 4;                 // [2]: S of tile A / B computed
-  uint64_t* p_full = bars + 6;                 // [2]: P written (O rescaled)
-  uint64_t* o_full = bars + 8;                 // [2]: a unit's last P V done
-  uint64_t* o_empty = bars + 10;               // [2]: O read by the epilogue
-  uint64_t* stat_full = bars + 12;             // [2 parities][2 tiles]: a unit's row sums written
-  uint64_t* k_full = bars + 16;                // [kStages] each
+  // [3]: S computed, P written (O rescaled), of tile A, of B, and of A in B's
+  // columns (a unit with one tile).  The last has barriers of its own: every
+  // barrier is followed by one role through all its phases, or a wait's
+  // parity could stand for the phase before.
+  uint64_t* s_full = bars + 4;
+  uint64_t* p_full = bars + 7;
+  uint64_t* o_full = bars + 10;                // [2]: a unit's last P V done
+  uint64_t* o_empty = bars + 12;               // [2]: O read by the epilogue
+  uint64_t* stat_full = bars + 14;             // [2 parities][2 tiles]: a unit's row sums written
+  uint64_t* k_full = bars + 18;                // [kStages] each
   uint64_t* k_empty = k_full + P::kStages;
   uint64_t* v_full = k_empty + P::kStages;
   uint64_t* v_ready = v_full + P::kStages;     // rows past the last key zeroed
   uint64_t* v_empty = v_ready + P::kStages;
   uint64_t* f_full = v_empty + P::kStages;      // [kFeedSlots] each: the ring of units
   uint64_t* f_empty = f_full + kFeedSlots;
-  uint64_t* done_bar = f_empty + kFeedSlots;
+  uint64_t* o_step = f_empty + kFeedSlots;     // a P V of a unit with one tile done
+  uint64_t* done_bar = o_step + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(done_bar + 2);
-  static_assert(16 + 5 * P::kStages + 2 * kFeedSlots + 3 <= 64, "barrier area holds 64 words");
+  static_assert(18 + 5 * P::kStages + 2 * kFeedSlots + 4 <= 64, "barrier area holds 64 words");
   float2* stat = reinterpret_cast<float2*>(smem + P::kStat);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -123,6 +131,9 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       mbar_init(&f_full[s], 1);
       mbar_init(&f_empty[s], kFeedReaders);
     }
+    mbar_init(&s_full[2], 1);
+    mbar_init(&p_full[2], 128);
+    mbar_init(o_step, 1);
     mbar_init(done_bar, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -272,10 +283,49 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         if (more && !wait_for(&k_full[ks], kph, wc)) break;
         int y = 0;                         // the next S to issue
         bool ok = true;
+        const bool single = kOne && have && u.q0 + xg.tokens >= u.q1;
+        if (kOne && single) {
+          // One query tile: its S takes turns in the two buffers, S(j + 1)
+          // before P V(j), so that a step is as long as the softmax.
+          if (more) {
+            tc_fence_after();
+            if (leader) {
+              const uint32_t kd = k_lo + (uint32_t)(ks * (P::kTileBytes >> 4)), ts = tS((j + 1) & 1);
+#pragma unroll
+              for (int kk = 0; kk < DH / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * P::kChunk + (kk & 3) * 32) >> 4;
+                umma_lo(ts, q_lo + o, kd + o, idS, (uint32_t)kk);
+              }
+              umma_commit(&s_full[(j & 1) ? 0 : 2]);
+              if (nvalid <= kTile) umma_commit(&q_empty[0]);
+            }
+            y = 2;  // nothing is left to issue
+          }
+          const int b = (j & 1) ? 2 : 0;
+          ok = wait_for(&p_full[b], (pph >> b) & 1, wc);
+          pph ^= 1u << b;
+          if (j == 0) {
+            if (ok && (used & 1)) {
+              ok = wait_for(&o_empty[0], oph & 1, wc);
+              oph ^= 1u;
+            }
+            used |= 1u;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t vd = v_lo + (uint32_t)(vs * (P::kTileBytes >> 4)), ts = tS(j & 1);
+            const int steps = min(valid + 15, kTile) >> 4;
+#pragma unroll 4
+            for (int kk = 0; kk < steps; ++kk) umma_ts_lo(tO(0), ts + kk * 8, vd + kk * 128, idO, (uint32_t)(j + kk));
+            umma_commit(o_step);
+            if (!more) umma_commit(&o_full[0]);
+          }
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           if (!ok) break;
-          if (have && (x == 0 || u.q0 + xg.tokens < u.q1)) {
+          if (have && !single && (x == 0 || kOne || u.q0 + xg.tokens < u.q1)) {
             // O_x += P_x V in steps of 16 keys, once P is written and O_x free of the unit before
             ok = wait_for(&p_full[x], (pph >> x) & 1, wc);
             pph ^= 1u << x;
@@ -303,7 +353,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           }
           if (!next) continue;
           // At a unit's end S_A of the next one goes before this one's PV_B if its operands are here.
-          if (x == 0 && !more && have && !(mbar_test(&k_full[ks], kph) && mbar_test(&q_full[0], qph & 1))) continue;
+          if (x == 0 && !more && have && !single && !(mbar_test(&k_full[ks], kph) && mbar_test(&q_full[0], qph & 1))) continue;
 #pragma unroll 1
           for (; y <= x && ok; ++y) {
             if (y == 1 && !nb) break;
@@ -354,19 +404,24 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     // ---------------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2, sub = warp & 3, row = sub * 32 + lane;
     const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
-    const uint32_t tSx = tS(x) + lane_base, tOx = tO(x) + lane_base;
+    const uint32_t tOx = tO(x) + lane_base;
     const float scale_log2 = 1.4426950408889634f * rsqrtf((float)DH);
-    uint32_t sc = 0, un = 0;
+    uint32_t sph = 0, un = 0;  // phases of s_full: bit by barrier
+    uint32_t ones = 0;         // steps of units with one tile so far
     bool ok = true;
     while (ok && feed.next<true>(u, wc)) {
-      const int n = ((u.k1 - u.k0 + kTile - 1) / kTile);
-      if (n == 0 || u.q0 + x * xg.tokens >= u.q1) continue;
+      const int n = (u.k1 - u.k0 + kTile - 1) / kTile;
+      const bool alone = u.q0 + xg.tokens >= u.q1, single = kOne && alone;  // tile A takes turns in both buffers
+      if (n == 0 || (alone && x == 1)) continue;
       float m_run = -INFINITY;
       uint64_t l2 = f2_pack(0.f, 0.f);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
-        if (!wait_for(&s_full[x], sc & 1, wc)) { ok = false; break; }
-        ++sc;
+        const int odd = single ? j & 1 : 0;
+        const int buf = odd ? 2 : x;
+        const uint32_t tSx = tS(x + odd) + lane_base;
+        if (!wait_for(&s_full[buf], (sph >> buf) & 1, wc)) { ok = false; break; }
+        sph ^= 1u << buf;
         tc_fence_after();
         const int valid = u.k1 - u.k0 - j * kTile;
         if (valid < kTile) {
@@ -449,6 +504,11 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           }
         }
         l2 = f2_add(l2, f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])));
+        if (single) {  // S(j) does not say that P V(j - 1) is done, as it does with two tiles
+          if (ones > 0 && !wait_for(o_step, (ones - 1) & 1, wc)) { ok = false; break; }
+          ++ones;
+          tc_fence_after();
+        }
         if (rescale) {
 #pragma unroll 1
           for (int c = 0; c < DH; c += 16) {
@@ -462,7 +522,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        mbar_arrive(&p_full[buf]);
       }
       if (!ok) break;
       float l0, l1;
@@ -638,14 +698,15 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
     pl = reinterpret_cast<float*>(ws);
     po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 4, 256));
   }
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(cross_fwd_kernel<DH>, P::kBytes, c.device, &allowed);
+  const bool one = a.N <= (int64_t)a.S * x.tokens;
+  static std::atomic<uint64_t> allowed[2];
+  const auto kernel = one ? cross_fwd_kernel<DH, true> : cross_fwd_kernel<DH, false>;
+  cudaError_t e = allow_smem(kernel, P::kBytes, c.device, &allowed[one]);
   if (e != cudaSuccess) return e;
   const int64_t units = places_most(a.N, 2 * x.tokens, a.S) * x.splits * x.heads;
   const unsigned grid = (unsigned)std::min<int64_t>(units, c.num_sms);
   set_steps(&x, grid);
-  cross_fwd_kernel<DH><<<grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, po, pl, a.withhold, c.status,
-                                                                 (unsigned long long)c.wait_ns);
+  kernel<<<grid, kXThreads, P::kBytes, c.stream>>>(m, a, x, po, pl, a.withhold, c.status, (unsigned long long)c.wait_ns);
   *launches = 1;
   if ((e = cudaGetLastError()) != cudaSuccess || x.splits == 1) return e;
   cross_join_kernel<DH><<<(unsigned)ceil_div(a.N * a.H, 8), 256, 0, c.stream>>>(a, x.splits, po, pl, c.status);

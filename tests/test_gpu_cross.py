@@ -158,6 +158,7 @@ def test_one_segment(N, L, H, Hk, d):
 
 
 SEGS = {
+    "one_and_two_tiles": ([100, 300, 1, 129, 128, 200, 5], [300, 129, 500, 100, 640, 128, 257]),
     "ragged": ([130, 0, 1, 300, 7, 256], [5, 64, 0, 257, 128, 33]),
     "singles": ([1] * 9, [1, 2, 0, 128, 129, 300, 17, 0, 64]),
     "empty": ([3, 0, 5], [0, 0, 0]),
@@ -172,6 +173,14 @@ SEGS = {
 @pytest.mark.parametrize("name", sorted(SEGS))
 def test_segments(name, d, H, Hk, edge, padded):
     check(*SEGS[name], H, Hk, d, seed=edge, edge=edge, padded=padded)
+
+
+@pytest.mark.parametrize("heads", [12, 16])
+def test_many_units_of_every_kind_on_each_sm(heads):
+    """More units than SMs, with one query tile and with two, of no to six key tiles, following one another."""
+    rng = np.random.default_rng(heads)
+    check(list(rng.integers(0, 420, 60)), list(rng.integers(0, 700, 60)), heads, heads // 4, 64)
+    check(list(rng.integers(0, 300, 40)), list(rng.integers(0, 300, 40)), heads, heads, 128)
 
 
 @pytest.mark.parametrize("layout", ["packed", "head_major", "head_rows", "wide"])
@@ -189,9 +198,10 @@ def test_matched_keys(peak):
     check([2], [3000], 2, 2, 64, peak=peak)
 
 
-def test_growing_scores():
+@pytest.mark.parametrize("N", [60, 200])
+def test_growing_scores(N):
     """Keys sorted by their score: every tile's maximum is above the last one's by more than 2^8."""
-    c = Case([200], [900], 1, 1, 128)
+    c = Case([N], [900], 1, 1, 128)
     u = torch.zeros(128, device="cuda")
     u[0] = 1
     c.q = (c.q.float() * 0.1 + 8 * u).to(torch.bfloat16)
