@@ -544,8 +544,8 @@ moga_status moga_set_timing_events(int stage, void* begin, void* end);
 
 /* moga_debug_inject: failure-detection test hook, process-wide.
  *   0: off (default).
- *   1: in later attention calls (grouped, STGA, shot-aware, and the layers
- *      built on them), the attention kernel's loader withholds each CTA's
+ *   1: in later attention calls (grouped, STGA, shot-aware, the layers
+ *      built on them, and moga_cross_attn), the attention kernel's loader withholds each CTA's
  *      first K tile, so the MMA warp's bounded wait runs out: the kernel
  *      drains, frees its tensor memory and exits, and moga_sync_status()
  *      reports MOGA_ERR_TIMEOUT.  Nothing faults

@@ -856,15 +856,16 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
 
 // The sum of the shares' rows, for rows of a segment: of dQ ([N, H], one
 // tensor a share), or of dV and dK ([L, H_kv], two; blockIdx.y picks one).
-// Eight threads share a row's piece, each every eighth share, in a fixed order.
+// blockDim.y threads (up to eight) share a row's piece, each every
+// blockDim.y-th share, in a fixed order.
 template <int DH>
 __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossArgs a, bool keys, int splits,
                                                         const float* __restrict__ part) {
-  __shared__ float4 lane_sum[8][32][2];
+  __shared__ float4 lane_sum[256][2];
   if (!segments_ok(a, nullptr)) return;
   const int heads = keys ? a.Hkv : a.H;
   const int64_t pieces = (keys ? a.L : a.N) * heads * (DH / 8);
-  const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t row = i / (DH / 8) / heads;
   bool inside = i < pieces;
   if (!keys) {
@@ -883,19 +884,19 @@ __global__ void __launch_bounds__(256) cross_sum_kernel(const CrossArgs a, bool 
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
   if (inside) {
 #pragma unroll 4
-    for (int s = threadIdx.y; s < splits; s += 8) {
+    for (int s = threadIdx.y; s < splits; s += blockDim.y) {
       const float4 u = *reinterpret_cast<const float4*>(p + s * step), v = *reinterpret_cast<const float4*>(p + s * step + 4);
       x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
       y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
     }
   }
-  lane_sum[threadIdx.y][threadIdx.x][0] = x;
-  lane_sum[threadIdx.y][threadIdx.x][1] = y;
+  const int me = threadIdx.y * blockDim.x + threadIdx.x;
+  lane_sum[me][0] = x;
+  lane_sum[me][1] = y;
   __syncthreads();
   if (threadIdx.y != 0 || !inside) return;
-#pragma unroll
-  for (int k = 1; k < 8; ++k) {
-    const float4 u = lane_sum[k][threadIdx.x][0], v = lane_sum[k][threadIdx.x][1];
+  for (int k = 1; k < (int)blockDim.y; ++k) {
+    const float4 u = lane_sum[me + k * blockDim.x][0], v = lane_sum[me + k * blockDim.x][1];
     x.x += u.x, x.y += u.y, x.z += u.z, x.w += u.w;
     y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
   }
@@ -965,7 +966,9 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
     return e;
   auto sum = [&](bool keys, int splits, const float* part) {
     const int64_t n = (keys ? a.L * a.Hkv : a.N * a.H) * (DH / 8);
-    cross_sum_kernel<DH><<<dim3((unsigned)ceil_div(n, 32), keys ? 2 : 1), dim3(32, 8), 0, c.stream>>>(a, keys, splits, part);
+    const int ny = splits >= 8 ? 8 : splits >= 4 ? 4 : 2;
+    cross_sum_kernel<DH><<<dim3((unsigned)ceil_div(n, 256 / ny), keys ? 2 : 1), dim3(256 / ny, ny), 0, c.stream>>>(
+        a, keys, splits, part);
     ++*launches;
     return cudaGetLastError();
   };

@@ -310,6 +310,27 @@ def test_other_streams_and_replayed_graphs():
     moga.sync_status(ws)
 
 
+@pytest.mark.parametrize("N,L", [(500, 300), (5, 3000)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(N, L):
+    """The library's test hook withholds each CTA's first K tile: the bounded waits run out, nothing hangs."""
+    lib = moga.get_lib()
+    c = Case([N], [L], 2, 2, 128)
+    ws = moga.workspace(moga.cross_attn_workspace_size(c.q, c.k), "cuda")
+    old = lib.moga_set_wait_limit_ns(50_000_000)
+    try:
+        assert lib.moga_debug_inject(1) == 0
+        moga.cross_attn(*c.in_place, ws=ws)
+        with pytest.raises(moga.MogaError) as e:
+            moga.sync_status(ws)
+        assert e.value.status == TIMEOUT
+    finally:
+        lib.moga_debug_inject(0)
+        lib.moga_set_wait_limit_ns(old)
+    moga.sync_status(ws)
+    check_forward(c, ws=ws)
+    moga.sync_status(ws)
+
+
 @pytest.mark.parametrize("layout", ["dense", "views", "broadcast"])
 def test_autograd(layout):
     """The function's gradients against 64-bit autograd of the formula."""
