@@ -133,6 +133,20 @@ __device__ __forceinline__ void write_row(uint32_t taddr, float f, bool keep, bo
   }
 }
 
+// p[0], p[1] = 2^(p scale + nl), in place.
+__device__ __forceinline__ void exp2_pair(float* p, uint64_t sc2, uint64_t nl2) {
+  float x, y;
+  f2_unpack(f2_fma(f2_pack(p[0], p[1]), sc2, nl2), x, y);
+  p[0] = fast_exp2(x);
+  p[1] = fast_exp2(y);
+}
+// P (dP - D) of two columns, in bf16.
+__device__ __forceinline__ uint32_t ds_pair(const float* p, const float* d, uint64_t md2) {
+  float x, y;
+  f2_unpack(f2_mul(f2_pack(p[0], p[1]), f2_add(f2_pack(d[0], d[1]), md2)), x, y);
+  return pack_bf16x2(x, y);
+}
+
 // ------------------------------------------------------------------ dQ
 template <int DH>
 __global__ void __launch_bounds__(kXThreads, 1)
@@ -385,34 +399,37 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
         if (!wait_for(&s_full[t & 1], (t >> 1) & 1, wc)) { ok = false; break; }
         tc_fence_after();
         const uint32_t ts = tS(t) + at;
-        float p[64];
-        tmem_ld32(ts, p);
-        tmem_ld32(ts + 32, p + 32);
-        tmem_ld_wait();
+        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nl2 = f2_pack(nl, nl);
+        // 32 columns at a time, in one loop body: unrolled over both halves
+        // the code that runs did not fit the instruction cache.
+        auto load_p = [&](int c, float* p) {
+          tmem_ld32(ts + c, p);
+          tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 64; ++e) p[e] = fast_exp2(fmaf(p[e], scale_log2, nl));
-        const int valid = u.k1 - k - 64 * wg;
-        if (valid < 64) {
+          for (int e = 0; e < 32; e += 2) exp2_pair(p + e, sc2, nl2);
+          const int valid = u.k1 - k - 64 * wg - c;
+          if (valid < 32) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e) p[e] = e < valid ? p[e] : 0.0f;
-        }
-        if (!wait_for(d_full, t & 1, wc)) { ok = false; break; }
-        tc_fence_after();
+            for (int e = 0; e < 32; ++e) p[e] = e < valid ? p[e] : 0.0f;
+          }
+        };
         if (flag & 2) {
           // One tile holds all of the row's keys: D = sum_j P_ij dP_ij, in
           // fp32.  From O, which is rounded to bf16, it would be the largest
           // error of the gradients where few keys make O as large as V.
+          if (!wait_for(d_full, t & 1, wc)) { ok = false; break; }
+          tc_fence_after();
           float sum = 0.0f;
 #pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
-            float d[32];
+            float p[32], d[32];
+            load_p(c, p);
             tmem_ld32(tD + at + c, d);
             tmem_ld_wait();
+            const int valid = u.k1 - k - 64 * wg - c;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float pe = c ? p[32 + e] : p[e];
-              if (c + e < valid) sum = fmaf(pe, d[e], sum);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (e < valid) sum = fmaf(p[e], d[e], sum);
           }
           atomicAdd(mine + kTile, sum);  // 0 and two terms: the same in either order
           mbar_arrive(sum_bar);
@@ -424,21 +441,28 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
           if (wg == 0 && tok < u.q1)
             a.dsum[(int64_t)((u.g << xg.log2r) + (row & (xg.r - 1))) * a.N + tok] = D;
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float d[32];
-          tmem_ld32(tD + at + 32 * c, d);
+        const uint64_t md2 = f2_pack(-D, -D);
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          float p[32], d[32];
+          load_p(c, p);
+          if (c == 0 && !(flag & 2)) {
+            ok = wait_for(d_full, t & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          tmem_ld32(tD + at + c, d);
           tmem_ld_wait();
-          if (c == 1) {
+          if (c > 0) {
             tc_fence_before();
             mbar_arrive(dp_free);
           }
           uint32_t pk[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            pk[e] = pack_bf16x2(p[32 * c + 2 * e] * (d[2 * e] - D), p[32 * c + 2 * e + 1] * (d[2 * e + 1] - D));
-          tmem_st16u(ts + 16 * c, pk);
+          for (int e = 0; e < 16; ++e) pk[e] = ds_pair(p + 2 * e, d + 2 * e, md2);
+          tmem_st16u(ts + c / 2, pk);
         }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[t & 1]);
@@ -484,15 +508,15 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
           const __nv_bfloat16 *px = static_cast<const __nv_bfloat16*>(a.dout) + o,
                               *py = static_cast<const __nv_bfloat16*>(a.out) + o;
 #pragma unroll 1
-          for (int c = 0; c < DH; c += 64) {
-            uint32_t x[32], y[32];
+          for (int c = 0; c < DH; c += 32) {
+            uint32_t x[16], y[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               load32(x + 8 * i, px + c + 16 * i);
               load32(y + 8 * i, py + c + 16 * i);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16; ++i) {
               D = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), D);
               D = fmaf(__uint_as_float(x[i] & 0xffff0000u), __uint_as_float(y[i] & 0xffff0000u), D);
             }
@@ -548,7 +572,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 34);
   float* vec1 = reinterpret_cast<float*>(smem + P::kVec);  // [3][128]: -lse log2 e
-  float* vec2 = vec1 + 3 * kTile;                          // [2][128]: D
+  float* vec2 = vec1 + 3 * kTile;                          // [2][128]: -D
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 33; ++i) {
@@ -663,7 +687,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
           const int r = lane + 32 * i;
           const int64_t at = (int64_t)(head_of(g, loop) + (r & (xg.r - 1))) * a.N + tok + (r >> xg.log2r);
           lv[i] = r < rows ? -a.lse[at] * kLog2e : -INFINITY;
-          dv[i] = r < rows ? a.dsum[at] : 0.0f;
+          dv[i] = r < rows ? -a.dsum[at] : 0.0f;
         }
       };
 #pragma unroll 1
@@ -771,19 +795,18 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
         if (!ok) break;
         tc_fence_after();
         const uint32_t ts = tS(t) + at;
-        const float4* nl = reinterpret_cast<const float4*>(vec1 + (t % 3) * kTile + 64 * wg);
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(vec1 + (t % 3) * kTile + 64 * wg);
         float p[64];
         tmem_ld32(ts, p);
         tmem_ld32(ts + 32, p + 32);
         tmem_ld_wait();
         // Columns past the last query: zeroed rows of Q and -inf make P 0.
+        const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float4 v = nl[e];
-          p[4 * e] = fast_exp2(fmaf(p[4 * e], scale_log2, v.x));
-          p[4 * e + 1] = fast_exp2(fmaf(p[4 * e + 1], scale_log2, v.y));
-          p[4 * e + 2] = fast_exp2(fmaf(p[4 * e + 2], scale_log2, v.z));
-          p[4 * e + 3] = fast_exp2(fmaf(p[4 * e + 3], scale_log2, v.w));
+          const ulonglong2 v = nl[e];  // four columns
+          exp2_pair(p + 4 * e, sc2, v.x);
+          exp2_pair(p + 4 * e + 2, sc2, v.y);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -795,7 +818,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
         ok = wait_for(d_full, t & 1, wc) && wait_for(&y2_ready[t % 2], (t / 2) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const float4* dd = reinterpret_cast<const float4*>(vec2 + (t % 2) * kTile + 64 * wg);
+        const ulonglong2* dd = reinterpret_cast<const ulonglong2*>(vec2 + (t % 2) * kTile + 64 * wg);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float d[32];
@@ -808,10 +831,9 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 v = dd[8 * c + e];
-            const float* q = p + 32 * c + 4 * e;
-            pk[2 * e] = pack_bf16x2(q[0] * (d[4 * e] - v.x), q[1] * (d[4 * e + 1] - v.y));
-            pk[2 * e + 1] = pack_bf16x2(q[2] * (d[4 * e + 2] - v.z), q[3] * (d[4 * e + 3] - v.w));
+            const ulonglong2 v = dd[8 * c + e];
+            pk[2 * e] = ds_pair(p + 32 * c + 4 * e, d + 4 * e, v.x);
+            pk[2 * e + 1] = ds_pair(p + 32 * c + 4 * e + 2, d + 4 * e + 2, v.y);
           }
           tmem_st16u(ts + 32 + 16 * c, pk);
         }
