@@ -632,6 +632,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       }
     }
     fill_rows<DH>(a, a.out, a.lse, (int64_t)blockIdx.x * 128 + threadIdx.x - 384, (int64_t)gridDim.x * 128);
+    if (xg.splits == 1) empty_segments<DH>(a, a.out, a.lse, blockIdx.x * 4 + warp - 12, gridDim.x * 4);
   }
   tc_fence_before();
   __syncthreads();

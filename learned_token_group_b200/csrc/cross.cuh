@@ -208,7 +208,29 @@ struct Walk {
     const int lane = threadIdx.x & 31;
     seg = Seg{0, 0, 0, 0};
     if (chunk + lane < a.S) seg = segment(a, chunk + lane);
+    if (a.S > 1) {
+      // The 32 segments by the length of their units, longest first: units
+      // are dealt in turn, and the last, partial round is then of short ones.
+      // Every other 32 the other way, so that long ones do not meet long ones.
+      const int len = by_keys ? seg.q1 - seg.q0 : seg.k1 - seg.k0, cost = (chunk & 32) ? -len : len;
+      int rank = 0, src = lane;
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const int c = __shfl_sync(0xffffffffu, cost, j);
+        rank += c > cost || (c == cost && j < lane);
+      }
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j)
+        if (__shfl_sync(0xffffffffu, rank, j) == lane) src = j;
+      seg = Seg{__shfl_sync(0xffffffffu, seg.q0, src), __shfl_sync(0xffffffffu, seg.q1, src),
+                __shfl_sync(0xffffffffu, seg.k0, src), __shfl_sync(0xffffffffu, seg.k1, src)};
+    }
     n = ((by_keys ? seg.k1 - seg.k0 : seg.q1 - seg.q0) + per - 1) / per;
+    // Queries without keys are no units (empty_segments sets their rows): the
+    // issuing warp looks for the next unit with keys before it has finished
+    // this one, and would wait for ever behind a ring full of others.  With
+    // shares a CTA has one unit, and the join wants a word from each.
+    if (!by_keys && x.splits == 1 && seg.k1 <= seg.k0) n = 0;
     incl = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -277,6 +299,28 @@ __device__ __forceinline__ void fill_rows(const CrossArgs& a, void* out, float* 
     const int64_t rest = i - r * a.H * (DH / 8);
     static_cast<uint4*>(out)[tok * a.H * (DH / 8) + rest] = make_uint4(0, 0, 0, 0);
     if (lse && rest % (DH / 8) == 0) lse[rest / (DH / 8) * a.N + tok] = -INFINITY;
+  }
+}
+
+// The rows of segments without keys: 0, and lse = -inf where it is given.
+// One warp of `warps` in the grid.
+template <int DH>
+__device__ __forceinline__ void empty_segments(const CrossArgs& a, void* out, float* lse, int64_t warp, int64_t warps) {
+  const int lane = threadIdx.x & 31;
+  for (int base = 0; base < a.S; base += 32) {
+    Seg g{0, 0, 0, 0};
+    if (base + lane < a.S) g = segment(a, base + lane);
+    unsigned empty = __ballot_sync(0xffffffffu, g.q1 > g.q0 && g.k1 <= g.k0);
+    for (; empty; empty &= empty - 1) {
+      const int src = __ffs(empty) - 1;
+      const int q0 = __shfl_sync(0xffffffffu, g.q0, src), q1 = __shfl_sync(0xffffffffu, g.q1, src);
+      for (int64_t tok = q0 + warp; tok < q1; tok += warps) {
+        uint4* row = static_cast<uint4*>(out) + tok * a.H * (DH / 8);
+        for (int i = lane; i < a.H * (DH / 8); i += 32) row[i] = make_uint4(0, 0, 0, 0);
+        if (lse)
+          for (int h = lane; h < a.H; h += 32) lse[(int64_t)h * a.N + tok] = -INFINITY;
+      }
+    }
   }
 }
 

@@ -534,6 +534,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
     }
     if (ok && pending) finish();
     fill_rows<DH>(a, a.dq, nullptr, (int64_t)blockIdx.x * 128 + threadIdx.x - 384, (int64_t)gridDim.x * 128);
+    if (xg.splits == 1) empty_segments<DH>(a, a.dq, nullptr, blockIdx.x * 4 + warp - 12, gridDim.x * 4);
   }
   tc_fence_before();
   __syncthreads();

@@ -183,6 +183,12 @@ def test_many_units_of_every_kind_on_each_sm(heads):
     check(list(rng.integers(0, 300, 40)), list(rng.integers(0, 300, 40)), heads, heads, 128)
 
 
+def test_many_queries_without_keys():
+    """More units without keys than a CTA's ring holds, behind, before and between others."""
+    check([300, 9000, 200, 9000, 130, 9000], [200, 0, 300, 0, 129, 0], 12, 12, 64)
+    check([9000, 300], [0, 200], 12, 12, 64)
+
+
 @pytest.mark.parametrize("layout", ["packed", "head_major", "head_rows", "wide"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_layouts(layout, d):
