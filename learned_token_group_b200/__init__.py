@@ -728,6 +728,7 @@ class QkNormRopeFunction(torch.autograd.Function):
         return qk_norm_rope(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, w_q, w_k, table, positions = ctx.saved_tensors
         axes, grid, token0, eps, halves = ctx.args
@@ -832,7 +833,9 @@ def cross_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
 class CrossAttnFunction(torch.autograd.Function):
     """``cross_attn`` under torch.autograd: out = CrossAttnFunction.apply(q, k,
     v, q_offsets, kv_offsets, kv_lens); q, k and v get gradients.  The inputs
-    may be views; those the kernels cannot read in place are copied."""
+    may be views; those the kernels cannot read in place are copied.  To put a
+    training step into a CUDA graph, capture ``cross_attn`` and
+    ``cross_attn_backward`` themselves."""
 
     @staticmethod
     def forward(ctx, q, k, v, q_offsets=None, kv_offsets=None, kv_lens=None):
@@ -842,6 +845,7 @@ class CrossAttnFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, *seg = ctx.saved_tensors
         dout = dout.to(torch.bfloat16).contiguous()

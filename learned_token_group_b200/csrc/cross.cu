@@ -194,6 +194,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       // -------------------------------------------------------------- units, and their query tiles
       if (lane == 0) tma_prefetch_desc(&m.q);
       const uint64_t once = l2_policy_evict_first();
+      const WaitCtx wu = unit_wait(wc);
       uint32_t n0 = 0, n1 = 0;  // tiles A, B loaded
       Walk it(a, xg, 2 * xg.tokens, false);
       while (true) {
@@ -203,16 +204,16 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         take_share(u.k0, u.k1, kTile, u.split, xg.splits);
         int go = 1;
         if (lane == 0) {
-          go = feed.put(u, more ? 1 : 0, wc);
+          go = feed.put(u, more ? 1 : 0, wu);
           if (go && more && u.k1 > u.k0) {
             const int head = u.g << xg.log2r;
-            go = wait_for(&q_empty[0], (n0 & 1) ^ 1, wc);
+            go = wait_for(&q_empty[0], (n0 & 1) ^ 1, wu);
             if (go) {
               load_tile<DH>(&m.q, m.qv, &q_full[0], smem + P::kQ, xg.r, head, u.q0, once);
               ++n0;
             }
             if (go && u.q0 + xg.tokens < u.q1) {
-              go = wait_for(&q_empty[1], (n1 & 1) ^ 1, wc);
+              go = wait_for(&q_empty[1], (n1 & 1) ^ 1, wu);
               if (go) {
                 load_tile<DH>(&m.q, m.qv, &q_full[1], smem + P::kQ + P::kTileBytes, xg.r, head, u.q0 + xg.tokens, once);
                 ++n1;
@@ -536,12 +537,13 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     }
   } else {
     // ---------------------------------------------------------------- epilogue
+    const WaitCtx wu = unit_wait(wc);
     const int sub = warp & 3, row = sub * 32 + lane;
     const uint32_t lane_base = (uint32_t)(sub * 32) << 16;
     uint8_t* stage = smem + P::kStage + sub * 4096;
     uint32_t un0 = 0, un1 = 0;  // units of tile A, B
     bool ok = true;
-    while (ok && feed.next<true, 100>(u, wc)) {
+    while (ok && feed.next<true, 100>(u, wu)) {
       const bool keys = u.k1 > u.k0;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
@@ -550,8 +552,8 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         float2 st = make_float2(0.0f, -INFINITY);
         if (keys) {
           const uint32_t n = x ? un1++ : un0++;
-          if (!wait_for<100>(&stat_full[(n & 1) * 2 + x], (n >> 1) & 1, wc) ||
-              !wait_for<20>(&o_full[x], n & 1, wc)) { ok = false; break; }
+          if (!wait_for<100>(&stat_full[(n & 1) * 2 + x], (n >> 1) & 1, wu) ||
+              !wait_for<20>(&o_full[x], n & 1, wu)) { ok = false; break; }
           tc_fence_after();
           st = stat[(n & 1) * 2 * kTile + x * kTile + row];
         }
@@ -700,9 +702,8 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
     po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 4, 256));
   }
   const bool one = a.N <= (int64_t)a.S * x.tokens;
-  static std::atomic<uint64_t> allowed[2];
   const auto kernel = one ? cross_fwd_kernel<DH, true> : cross_fwd_kernel<DH, false>;
-  cudaError_t e = allow_smem(kernel, P::kBytes, c.device, &allowed[one]);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t units = places_most(a.N, 2 * x.tokens, a.S) * x.splits * x.heads;
   const unsigned grid = (unsigned)std::min<int64_t>(units, c.num_sms);

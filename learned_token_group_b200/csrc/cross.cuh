@@ -5,8 +5,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
-
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -65,7 +63,7 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, const Wait
     if (++n & 63u) continue;
     const uint32_t t = (uint32_t)(global_timer_ns() >> 10);  // about a microsecond
     if (n == 64) t0 = t;
-    if (t - t0 > (uint32_t)(c.limit_ns >> 10)) {
+    if (t - t0 > (uint32_t)min((unsigned long long)(c.limit_ns >> 10), 0xfffffffeull)) {
       *c.abort_flag = 1;
       if (c.status) atomicOr(c.status, DEV_TIMEOUT);
     }
@@ -75,6 +73,14 @@ __device__ __noinline__ bool wait_more(uint32_t bar, uint32_t parity, const Wait
 template <int kSleep = 0>
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const WaitCtx& c) {
   return mbar_try_wait(bar, parity) || wait_more<kSleep>(smem_u32(bar), parity, c);
+}
+
+// For waits that last as long as a unit does (the writers of its results, and
+// the walk, which is a unit ahead): the roles that step through the unit bound
+// it, and their abort flag ends these too.
+__device__ __forceinline__ WaitCtx unit_wait(WaitCtx c) {
+  c.limit_ns = c.limit_ns < (1ull << 33) ? c.limit_ns * 256 : c.limit_ns;
+  return c;
 }
 
 __device__ __forceinline__ void tmem_st1(uint32_t taddr, float v) {
@@ -387,16 +393,6 @@ inline int pack_of(const CrossArgs& a) {
   const int r = a.H / a.Hkv;
   if (a.N == 0 || r < 2 || r > 64 || (r & (r - 1))) return 1;
   return a.q_sn >= (a.H - 1) * a.q_sh + a.d_h && a.q_sn % a.q_sh == 0 ? r : 1;
-}
-
-// The kernel's shared memory, allowed once per device.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes, int device, std::atomic<uint64_t>* done) {
-  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
-  if (bit && (done->load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
-  return e;
 }
 
 inline void set_steps(XGrid* x, int64_t grid) {

@@ -233,6 +233,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- units, their Q and dO tiles
+    const WaitCtx wu = unit_wait(wc);
     const uint64_t once = l2_policy_evict_first();
     uint32_t n = 0, nd = 0;
     Walk it(a, xg, xg.tokens, false);
@@ -251,13 +252,13 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
           prefetch_tile<DH>(&m.out, m.dv, xg.r, head, u.q0);
           prefetch_tile<DH>(&m.dout, m.dv, xg.r, head, u.q0);
         }
-        go = feed.put(u, flag, wc);
+        go = feed.put(u, flag, wu);
         if (go && more && u.k1 > u.k0) {
-          go = wait_for(q_empty, (n & 1) ^ 1, wc);
+          go = wait_for(q_empty, (n & 1) ^ 1, wu);
           if (go) {
             load_tile<DH>(&m.q, m.qv, q_full, smem + P::kQ, xg.r, head, u.q0, once);
             ++n;
-            go = wait_for(do_empty, (nd & 1) ^ 1, wc);
+            go = wait_for(do_empty, (nd & 1) ^ 1, wu);
           }
           if (go) {
             load_tile<DH>(&m.dout, m.dv, do_full, smem + P::kDO, xg.r, head, u.q0, once);
@@ -471,6 +472,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
     }
   } else {
     // ---------------------------------------------------------------- D a unit ahead, and the results
+    const WaitCtx wu = unit_wait(wc);
     const int sub = warp & 3, row = sub * 32 + lane;
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
     uint32_t un = 0, on = 0;
@@ -484,7 +486,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
                     part ? part + (int64_t)w.split * a.N * a.H * DH + o : nullptr);
     };
     auto finish = [&]() {  // the unit before
-      if (!wait_for<100>(acc_full, on & 1, wc)) return false;
+      if (!wait_for<100>(acc_full, on & 1, wu)) return false;
       ++on;
       tc_fence_after();
       write(pu, true);
@@ -493,7 +495,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
       return true;
     };
     int flag;
-    while (ok && (flag = feed.next_flag<true, 100>(u, wc)) != 0) {
+    while (ok && (flag = feed.next_flag<true, 100>(u, wu)) != 0) {
       const bool keys = u.k1 > u.k0;
       if (keys) {
         float* out = vec + (un & 1) * 2 * kTile;
@@ -642,6 +644,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
     }
   } else if (warp == 3) {
     // ---------------------------------------------------------------- units, their K and V tiles
+    const WaitCtx wu = unit_wait(wc);
     const uint64_t once = l2_policy_evict_first();
     uint32_t n = 0;
     Walk it(a, xg, kTile, true);
@@ -652,9 +655,9 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
       take_share(u.q0, u.q1, xg.tokens, u.split, xg.splits);
       int go = 1;
       if (lane == 0) {
-        go = feed.put(u, more ? 1 : 0, wc);
+        go = feed.put(u, more ? 1 : 0, wu);
         if (go && more && u.q1 > u.q0) {
-          go = wait_for(x_empty, (n & 1) ^ 1, wc);
+          go = wait_for(x_empty, (n & 1) ^ 1, wu);
           if (go) {
             // both tiles on one barrier: the second's bytes are added before the first phase can complete
             mbar_expect_tx(x_full, 2 * P::T);
@@ -845,14 +848,15 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
     }
   } else {
     // ---------------------------------------------------------------- the results
+    const WaitCtx wu = unit_wait(wc);
     const int sub = warp & 3, row = sub * 32 + lane;
     const uint32_t lanes = (uint32_t)(sub * 32) << 16;
     const int64_t rows = a.L * a.Hkv;
     uint32_t on = 0;
-    while (feed.next<true, 500>(u, wc)) {
+    while (feed.next<true, 500>(u, wu)) {
       const bool some = u.q1 > u.q0;
       if (some) {
-        if (!wait_for<500>(acc_full, on & 1, wc)) break;
+        if (!wait_for<500>(acc_full, on & 1, wu)) break;
         ++on;
         tc_fence_after();
       }
@@ -983,9 +987,8 @@ cudaError_t launch_bwd(const DevCtx& c, CrossArgs a, uint8_t* ws, int* launches)
          view_2d(&m.out, &m.dv, a.out, HD, DH, a.N, a.H, DH);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e;
-  static std::atomic<uint64_t> dq_allowed{0}, dkv_allowed{0};
-  if ((e = allow_smem(cross_dq_kernel<DH>, P::kBytes, c.device, &dq_allowed)) != cudaSuccess ||
-      (e = allow_smem(cross_dkv_kernel<DH>, P::kBytes, c.device, &dkv_allowed)) != cudaSuccess)
+  if ((e = cudaFuncSetAttribute(cross_dq_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess ||
+      (e = cudaFuncSetAttribute(cross_dkv_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kBytes)) != cudaSuccess)
     return e;
   auto sum = [&](bool keys, int splits, const float* part) {
     const int64_t n = (keys ? a.L * a.Hkv : a.N * a.H) * (DH / 8);
