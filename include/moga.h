@@ -431,7 +431,7 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
  *      [S], at most the distance to the next offset; NULL: all of it.
  *      Checked on the device: a violation skips all work and
  *      moga_sync_status() reports MOGA_ERR_DEVICE_CHECK.
- * Out: out bf16 [N, H, d_h], dense; lse fp32 [H, N] or NULL: the natural
+ * Out: out bf16 [N, H, d_h], dense, apart from the inputs; lse fp32 [H, N] or NULL: the natural
  *      log-sum-exp of each query's scaled scores.  A query whose segment has
  *      no keys gets out = 0 and lse = -inf.  Rows of no segment are left as
  *      they were (fill = 0) or set likewise (fill = 1).  Values of rows that no segment reads (padding) have no

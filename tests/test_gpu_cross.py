@@ -157,6 +157,52 @@ def test_one_segment(N, L, H, Hk, d):
     check([N], [L], H, Hk, d, seed=N + L)
 
 
+@pytest.mark.parametrize("H,Hk", [(64, 1), (128, 2), (128, 1), (5, 1), (12, 4), (32, 1)])
+def test_shared_key_heads(H, Hk):
+    """Tiles of all query heads of a key head (up to 64, a power of two), or of one at a time."""
+    check([9], [70], H, Hk, 64)
+    check([37, 0, 130], [200, 5, 19], H, Hk, 64)
+
+
+def test_a_thousand_segments():
+    rng = np.random.default_rng(3)
+    check(list(rng.integers(0, 5, 1024)), list(rng.integers(0, 40, 1024)), 4, 2, 64)
+    check(list(rng.integers(0, 5, 100)), list(rng.integers(0, 300, 100)), 2, 2, 128)
+
+
+def test_lengths_without_offsets():
+    """One segment whose keys end early: the same bits as without the rows behind, whatever they hold."""
+    c = Case([70], [90], 2, 2, 128)
+    c.k[50:], c.v[50:] = float("nan"), float("inf")
+    n = ints([50])
+    out, lse = moga.cross_attn(c.q, c.k, c.v, kv_lens=n, return_lse=True)
+    want, lse2 = moga.cross_attn(c.q, c.k[:50], c.v[:50], return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, lse2)
+    g = moga.cross_attn_backward(c.dout, c.q, c.k, c.v, out, lse, kv_lens=n)
+    h = moga.cross_attn_backward(c.dout, c.q, c.k[:50], c.v[:50], out, lse)
+    assert torch.equal(g["dq"], h["dq"])
+    for x in ("dk", "dv"):
+        assert torch.equal(g[x][:50], h[x]) and (g[x][50:] == 0).all()
+    out, lse = moga.cross_attn(c.q, c.k, c.v, kv_lens=ints([0]), return_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    g = moga.cross_attn_backward(c.dout, c.q, c.k, c.v, out, lse, kv_lens=ints([0]))
+    assert all((g[x] == 0).all() for x in ("dq", "dk", "dv"))
+
+
+def test_infinities_stay_in_their_rows():
+    """An infinite query makes its own row NaN, an infinite value its own channel infinite; the rest keeps its bits."""
+    c = Case([140], [200], 2, 2, 64)
+    want = moga.cross_attn(c.q, c.k, c.v)
+    q, v = c.q.clone(), c.v.clone()
+    q[5, 0, 3] = float("inf")
+    v[7, 1, 9] = float("inf")
+    got = moga.cross_attn(q, c.k, v)
+    assert torch.isnan(got[5, 0]).all() and torch.isinf(got[:, 1, 9]).all()
+    keep = torch.ones_like(got, dtype=torch.bool)
+    keep[5, 0] = keep[:, 1, 9] = False
+    assert torch.equal(got[keep], want[keep])
+
+
 SEGS = {
     "one_and_two_tiles": ([100, 300, 1, 129, 128, 200, 5], [300, 129, 500, 100, 640, 128, 257]),
     "ragged": ([130, 0, 1, 300, 7, 256], [5, 64, 0, 257, 128, 33]),
