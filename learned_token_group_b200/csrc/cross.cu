@@ -671,14 +671,22 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   float l = 0.0f, o[C] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float e = part_lse[s * rows + at];
-    if (e == -INFINITY) continue;
-    const float f = expf(e - m);
-    l += f;
-    const float* p = part_o + (s * rows + w) * DH + lane * C;
+  const float* p = part_o + w * DH + lane * C;
+  for (int base = 0; base < splits; base += 32) {
+    // 32 weights at a time, one a lane; the rows of the shares with keys
+    // then come in several at once
+    const float e = base + lane < splits ? part_lse[(base + lane) * rows + at] : -INFINITY;
+    const float f = e == -INFINITY ? 0.0f : expf(e - m);
+#pragma unroll 8
+    for (int s = 0; s < min(32, splits - base); ++s) {
+      const float g = __shfl_sync(0xffffffffu, f, s);
+      l += g;
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = fmaf(f, p[i], o[i]);
+      for (int i = 0; i < C; ++i) {
+        const float v = g > 0.0f ? p[(base + s) * rows * DH + i] : 0.0f;
+        o[i] = fmaf(g, v, o[i]);
+      }
+    }
   }
   store_row<C>(a.out, w * DH, lane, o, l > 0.0f ? 1.0f / l : 0.0f);
   if (a.lse && lane == 0) a.lse[at] = m + logf(l);
