@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moga {
 namespace {
@@ -141,17 +142,49 @@ __device__ __forceinline__ bool angles(const NormArgs& a, int64_t n, int l, floa
   return true;
 }
 
+// Turns the pairs of x by the angles (sign = 1) or back (-1), two products at
+// a time: (u, v) c + (-v, u) s, or over two pairs where a pair's channels are
+// four elements apart.
 template <bool kHalves>
 __device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const float (&s)[4], float sign) {
+  if (kHalves) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float& u = x[kHalves ? i : 2 * i];
-    float& v = x[kHalves ? i + 4 : 2 * i + 1];
-    const float sn = sign * s[i];
-    const float y = u * c[i] - v * sn;
-    v = u * sn + v * c[i];
-    u = y;
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t u = f2_pack(x[i], x[i + 1]), v = f2_pack(x[i + 4], x[i + 5]);
+      const uint64_t c2 = f2_pack(c[i], c[i + 1]), s2 = f2_pack(sign * s[i], sign * s[i + 1]);
+      const uint64_t m2 = f2_pack(-sign * s[i], -sign * s[i + 1]);
+      f2_unpack(f2_fma(v, m2, f2_mul(u, c2)), x[i], x[i + 1]);
+      f2_unpack(f2_fma(u, s2, f2_mul(v, c2)), x[i + 4], x[i + 5]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float u = x[2 * i], v = x[2 * i + 1];
+      const uint64_t y = f2_mul(f2_pack(u, v), f2_pack(c[i], c[i]));
+      f2_unpack(f2_fma(f2_pack(v, u), f2_pack(-sign * s[i], sign * s[i]), y), x[2 * i], x[2 * i + 1]);
+    }
   }
+}
+
+// Eight values as four packed pairs.
+struct Eight {
+  uint64_t p[4];
+  __device__ __forceinline__ explicit Eight(const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+  }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(p[i], x[2 * i], x[2 * i + 1]);
+  }
+};
+__device__ __forceinline__ float dot8(const Eight& a, const Eight& b) {
+  uint64_t t = f2_mul(a.p[0], b.p[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) t = f2_fma(a.p[i], b.p[i], t);
+  float x, y;
+  f2_unpack(t, x, y);
+  return x + y;
 }
 
 // Sum over the lanes that share a row.
@@ -206,6 +239,7 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_kernel(const NormAr
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;
+    const Eight w8(w);
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y[t]) + it.n * a.heads[t] * DH;
 #pragma unroll
     for (int u = 0; u < kRows<T>; ++u) {
@@ -213,12 +247,12 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_kernel(const NormAr
       const int h = h0 + u * RPW;
       float v[8];
       values(raw[u], v);
-      float q = 0.0f;
+      Eight x8(v);
+      const float r = rsqrtf(row_sum<LPR>(dot8(x8, x8)) * (1.0f / DH) + a.eps);
+      const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-      const float r = rsqrtf(row_sum<LPR>(q) * (1.0f / DH) + a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= r * w[e];
+      for (int i = 0; i < 4; ++i) x8.p[i] = f2_mul(x8.p[i], f2_mul(r2, w8.p[i]));
+      x8.to(v);
       if (kRot) turn<kHalves>(v, c, s, 1.0f);
       if (h < a.heads[t]) store8<DH, kHalves>(y + h * DH, l, v);
     }
@@ -257,6 +291,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const No
     float w[8], dw[8] = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;
+    const Eight w8(w);
+    Eight dw8(dw);
     T* dx = static_cast<T*>(a.y[t]) + it.n * a.heads[t] * DH;
 #pragma unroll
     for (int u = 0; u < kRows<T>; ++u) {
@@ -266,24 +302,24 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const No
       values(raw[u], v);
       values(grad[u], g);
       if (kRot) turn<kHalves>(g, c, s, -1.0f);
-      float q = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-      const float r = rsqrtf(row_sum<LPR>(q) * (1.0f / DH) + a.eps);
+      Eight x8(v), g8(g);
+      const float r = rsqrtf(row_sum<LPR>(dot8(x8, x8)) * (1.0f / DH) + a.eps);
       const bool live = h < a.heads[t];  // a missing row's 0 * inf (eps = 0) must not reach dw
-      float m = 0.0f;
+      const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] *= r;
-        if (live) dw[e] = fmaf(g[e], v[e], dw[e]);
-        g[e] *= w[e];
-        m = fmaf(g[e], v[e], m);
+      for (int i = 0; i < 4; ++i) {
+        x8.p[i] = f2_mul(x8.p[i], r2);
+        if (live) dw8.p[i] = f2_fma(g8.p[i], x8.p[i], dw8.p[i]);
+        g8.p[i] = f2_mul(g8.p[i], w8.p[i]);
       }
-      m = row_sum<LPR>(m) * (1.0f / DH);
+      const float m = row_sum<LPR>(dot8(g8, x8)) * (-1.0f / DH);
+      const uint64_t m2 = f2_pack(m, m);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) g[e] = r * (g[e] - v[e] * m);
+      for (int i = 0; i < 4; ++i) g8.p[i] = f2_mul(r2, f2_fma(x8.p[i], m2, g8.p[i]));
+      g8.to(g);
       if (live) store8<DH, kHalves>(dx + h * DH, l, g);
     }
+    dw8.to(dw);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       acc[0][e] += t ? 0.0f : dw[e];
