@@ -527,11 +527,13 @@ class MogaFunction(torch.autograd.Function):
 # microsecond each: attributes are read once, and messages made on failure.
 _BF16 = (torch.bfloat16,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
-_raw_stream = torch._C._cuda_getCurrentRawStream  # current_stream(dev).cuda_stream without its objects
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream(dev).cuda_stream without its objects
 
 
 @functools.lru_cache(maxsize=256)
 def _triple(a: int, b: int, c: int):
+    if not all(-1 << 31 <= x < 1 << 31 for x in (a, b, c)):  # ctypes would take them modulo 2^32
+        raise ValueError(f"axes and grid must fit 32 bits, got {(a, b, c)}")
     return (ctypes.c_int * 3)(a, b, c)
 
 
@@ -643,6 +645,8 @@ def _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halve
             raise ValueError("a table needs a grid or positions, one of them")
         axes = _triple(*map(int, axes))
         grid = None if grid is None else _triple(*map(int, grid))
+        if token0 < 0 or token0 >> 31:
+            raise ValueError(f"token0 must be the place of a token on the grid, got {token0}")
     elif grid is not None or positions is not None:
         raise ValueError("grid and positions need a table")
     else:

@@ -359,6 +359,17 @@ def test_refusals():
         moga.qk_norm_rope_backward(a["q"], a["k"].float(), **a)
 
 
+def test_numbers_past_32_bits_are_refused():
+    # 2^32 + 1 and 2^64 would come down as 1 and 0.
+    a, _ = make(10, 2, 2, 64, torch.bfloat16, "dense", "grid")
+    big = (1 << 32) + 1
+    for kw in (dict(grid=(big, *a["grid"][1:])), dict(axes=(big, 0, 0)), dict(token0=1 << 64), dict(token0=-1)):
+        with pytest.raises(ValueError, match="grid"):
+            moga.qk_norm_rope(**dict(a, **kw))
+    with pytest.raises(ValueError, match="32 bits"):
+        moga.rope_table(8, 64, (big, 0, 0))
+
+
 def test_offsets_past_32_bits():
     """Tokens 2^31 elements apart in one buffer (4 GB of bf16, mostly untouched)."""
     N, H, d = 4100, 4, 128
