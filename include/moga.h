@@ -433,8 +433,11 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
  *      moga_sync_status() reports MOGA_ERR_DEVICE_CHECK.
  * Out: out bf16 [N, H, d_h], dense, apart from the inputs; lse fp32 [H, N] or NULL: the natural
  *      log-sum-exp of each query's scaled scores.  A query whose segment has
- *      no keys gets out = 0 and lse = -inf.  Rows of no segment are left as
- *      they were (fill = 0) or set likewise (fill = 1).  Values of rows that no segment reads (padding) have no
+ *      no keys, or whose scores are all -inf, gets out = 0 and lse = -inf.
+ *      Scores are fp32 of any size: keys that a channel masks with -inf or the
+ *      type's lowest value weigh nothing beside ordinary ones.  Rows of no
+ *      segment are left as they were (fill = 0) or set as those without keys
+ *      (fill = 1).  Values of rows that no segment reads (padding) have no
  *      effect, infinities and NaN included.
  * Limits: d_h 64 or 128; N, L < 2^30; N * H, L * H_kv < 2^31; H a multiple
  * of H_kv; S <= 1024.

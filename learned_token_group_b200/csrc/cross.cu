@@ -35,23 +35,49 @@
 // power cap); x 128 keys: 0.24 ms, 4.8 TB/s.  Bound by the issue of products
 // (about 100 cycles an instruction against 64 of math) with long prompts, by
 // HBM and the epilogue with short ones.
-// With few units the key range is split over CTAs, which write O / l and lse in
-// fp32, and cross_join_kernel joins them.
+// With few units the key range is split over CTAs, which write O / l and (l, m)
+// in fp32, and cross_join_kernel joins them.
+//
+// P = exp2(S scale - fl(m scale)) in one fused step, m the running maximum of
+// the scores themselves.  The rounding of m scale is a factor of P that l shares;
+// but it passes 2^128 once m scale is past 2^32, and P would be infinite or 0.
+// Past kFar = 2^29 two scores that differ do so by |m| 2^-24 at least, 32 in the
+// exponent: the smaller one's weight is nothing in fp32, at half the scale too.
+// There the scale is a power of two, whose products are exact: P = 1 at the
+// maximum.  Only the row's two factors change; subtracting m from every S first
+// cost 1 to 4 %.  m starts at the lowest finite value, not at -inf: a tile of
+// scores of -inf gives P = 0, where -inf - -inf is NaN for all tiles behind it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "cross.cuh"
 
 namespace moga {
 namespace {
 
+constexpr float kFar = 536870912.0f;
+constexpr float kFarScale = 0.125f;  // the power of two below log2(e) / sqrt(64) and log2(e) / sqrt(128)
+
+// 2^((m - to) scale), to >= m: what a sum over P with m for reference takes for `to`.
+__device__ __forceinline__ float moved(float m, float to, float scale_log2) {
+  const float ms = m * scale_log2;
+  if (fabsf(ms) > kFar) return m == to ? 1.0f : 0.0f;
+  return fast_exp2(ms - to * scale_log2);
+}
+
 template <int C>
 __device__ __forceinline__ void store_row(void* base, int64_t at, int lane, const float (&x)[C], float f) {
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at + lane * C;
 #pragma unroll
   for (int i = 0; i < C; ++i) p[i] = __float2bfloat16(x[i] * f);
+}
+
+// Natural log-sum-exp of the scaled scores from l and m; -inf for l = 0.
+__device__ __forceinline__ float lse_of(float l, float m, int d_h) {
+  return (m * (1.4426950408889634f * rsqrtf((float)d_h)) + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int DH>
@@ -63,7 +89,7 @@ struct XPlan {
   static constexpr int kK = 2 * kTileBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kStage = kV + kStages * kTileBytes;  // epilogue: 4 KB per warp
-  static constexpr int kStat = kStage + 4 * 4096;    // [2 parities][2 tiles][128] of (1 / l, lse)
+  static constexpr int kStat = kStage + 4 * 4096;    // [2 parities][2 tiles][128] of (l, m)
   static constexpr int kBar = kStat + 2 * 2 * kTile * 8;
   static constexpr int kFeed = kBar + 512;           // ring of units
   static constexpr int kBytes = kFeed + kFeedSlots * 32 + 1024;
@@ -81,7 +107,7 @@ struct XMaps {
 // code it adds costs 4 %.
 template <int DH, bool kOne>
 __global__ void __launch_bounds__(kXThreads, 1)
-cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid xg, float* part_o, float* part_lse,
+cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid xg, float* part_o, float2* part_lm,
                  int withhold, int* status, unsigned long long wait_ns) {
   using P = XPlan<DH>;
   extern __shared__ uint8_t smem_raw[];
@@ -420,7 +446,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       const int n = (u.k1 - u.k0 + kTile - 1) / kTile;
       const bool alone = u.q0 + xg.tokens >= u.q1, single = kOne && alone;  // tile A takes turns in both buffers
       if (n == 0 || (alone && x == 1)) continue;
-      float m_run = -INFINITY;
+      float m_run = -FLT_MAX;
       uint64_t l2 = f2_pack(0.f, 0.f);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
@@ -468,25 +494,26 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           }
           mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        const float m_new = fmaxf(m_run, mx * scale_log2);
-        // The maximum moves, and O is rescaled, only when it grows by more
-        // than 2^8; P and l share the older one otherwise.
+        const float m_new = fmaxf(m_run, mx);
+        // The maximum moves, and O is rescaled, only when the exponent would
+        // pass 8; P and l share the older one otherwise.
         float alpha = 1.0f;
         bool rescale = false;
         if (j == 0) {
           m_run = m_new;
         } else {
-          const bool need = m_new > m_run + 8.0f;
+          const bool need = (m_new - m_run) * scale_log2 > 8.0f;
           rescale = __any_sync(0xffffffffu, need);
           if (need) {
-            alpha = fast_exp2(m_run - m_new);
+            alpha = moved(m_run, m_new, scale_log2);
             l2 = f2_mul(l2, f2_pack(alpha, alpha));
             m_run = m_new;
           }
         }
-        // P = 2^(S scale - m) to bf16, the operand's type: rounding it by 2^-9
-        // of itself keeps O within what its own bf16 holds.  l sums it unrounded.
-        const uint64_t sc2 = f2_pack(scale_log2, scale_log2), nm2 = f2_pack(-m_run, -m_run);
+        // P = 2^(S scale - m scale) to bf16, the operand's type: rounding it by 2^-8
+        // of itself at most is what O's own rounding may cost.  l sums it unrounded.
+        const float sc = fabsf(m_run * scale_log2) > kFar ? kFarScale : scale_log2, nm = -m_run * sc;
+        const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(nm, nm);
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
         for (int half = 0; half * 64 < min(valid, kTile); ++half) {  // P V stops at the last key's 16
@@ -537,7 +564,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       const float l = l0 + l1;
       // The slot of unit un + 2 is written only after the epilogue of unit un
       // has freed O, which P V of unit un + 1 waited for.
-      stat[(un & 1) * 2 * kTile + x * kTile + row] = make_float2(1.0f / l, (m_run + log2f(l)) * 0.6931471805599453f);
+      stat[(un & 1) * 2 * kTile + x * kTile + row] = make_float2(l, m_run);
       mbar_arrive(&stat_full[(un & 1) * 2 + x]);
       ++un;
     }
@@ -555,7 +582,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       for (int x = 0; x < 2; ++x) {
         const int tok0 = u.q0 + x * xg.tokens;
         if (tok0 >= u.q1) break;
-        float2 st = make_float2(0.0f, -INFINITY);
+        float2 st = make_float2(0.0f, -FLT_MAX);
         if (keys) {
           const uint32_t n = x ? un1++ : un0++;
           if (!wait_for<100>(&stat_full[(n & 1) * 2 + x], (n >> 1) & 1, wu) ||
@@ -571,8 +598,13 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         };
         int tok, h;
         const bool live = place(row, tok, h);
-        float* lse = part_lse ? part_lse + (int64_t)u.split * a.H * a.N : a.lse;
-        if (lse && live) lse[(int64_t)h * a.N + tok] = st.y;
+        if (part_o) {
+          if (live) part_lm[((int64_t)u.split * a.H + h) * a.N + tok] = st;
+        } else if (a.lse && live) {
+          a.lse[(int64_t)h * a.N + tok] = lse_of(st.x, st.y, DH);
+        }
+        // l is at least 2^-16, or 0 where every score is -inf: as without keys
+        st.x = st.x == 0.0f ? 0.0f : __fdividef(1.0f, st.x);
         if (part_o && !keys) continue;  // the join leaves a share without keys out
         const uint32_t to = tO(x) + lane_base;
         const int piece = lane & 7, sub8 = lane >> 3;
@@ -650,11 +682,13 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
   }
 }
 
-// out and lse from the splits' O / l and lse: out = sum_s exp(lse_s - lse) O_s.
-// One warp per (token, head) of a segment; a share without keys has lse = -inf.
+// out and lse from the shares' O_s = O / l and (l_s, m_s): with m the largest m_s
+// and w_s = l_s 2^((m_s - m) scale), out = sum_s w_s O_s / sum_s w_s.  One warp
+// per (token, head) of a segment; a share without keys has l = 0.  Two numbers
+// and not lse alone, which loses l where m is large.
 template <int DH>
 __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int splits, const float* __restrict__ part_o,
-                                                         const float* __restrict__ part_lse, int* status) {
+                                                         const float2* __restrict__ part_lm, int* status) {
   constexpr int C = DH / 32;
   if (!segments_ok(a, nullptr)) return;  // the kernel before reported it
   const int lane = threadIdx.x & 31;
@@ -666,8 +700,9 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
   if (!inside) inside = n >= a.q_off[0] && n < a.q_off[a.S];  // segments follow one another
   if (!inside) return;
   const int64_t rows = a.N * a.H, at = (int64_t)h * a.N + n;
-  float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lse[s * rows + at]);
+  const float scale_log2 = 1.4426950408889634f * rsqrtf((float)DH);
+  float m = -FLT_MAX;
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lm[s * rows + at].y);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   float l = 0.0f, o[C] = {};
@@ -675,8 +710,8 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
   for (int base = 0; base < splits; base += 32) {
     // 32 weights at a time, one a lane; the rows of the shares with keys
     // then come in several at once
-    const float e = base + lane < splits ? part_lse[(base + lane) * rows + at] : -INFINITY;
-    const float f = e == -INFINITY ? 0.0f : expf(e - m);
+    const float2 e = base + lane < splits ? part_lm[(base + lane) * rows + at] : make_float2(0.0f, m);
+    const float f = e.x * moved(e.y, m, scale_log2);
 #pragma unroll 8
     for (int s = 0; s < min(32, splits - base); ++s) {
       const float g = __shfl_sync(0xffffffffu, f, s);
@@ -688,8 +723,8 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
       }
     }
   }
-  store_row<C>(a.out, w * DH, lane, o, l > 0.0f ? 1.0f / l : 0.0f);
-  if (a.lse && lane == 0) a.lse[at] = m + logf(l);
+  store_row<C>(a.out, w * DH, lane, o, l == 0.0f ? 0.0f : 1.0f / l);
+  if (a.lse && lane == 0) a.lse[at] = lse_of(l, m, DH);
 }
 
 
@@ -710,10 +745,11 @@ cudaError_t launch_fwd(const DevCtx& c, const CrossArgs& a, uint8_t* ws, int* la
   ok = ok && (x.r > 1 ? make_tmap_heads(&m.q, a.q, DH, a.H, a.N, a.q_sh, a.q_sn, x.r, x.tokens)
                       : view_2d(&m.q, &m.qv, a.q, a.q_sn, a.q_sh, a.N, a.H, DH));
   if (!ok) return cudaErrorInvalidValue;
-  float *po = nullptr, *pl = nullptr;
+  float* po = nullptr;
+  float2* pl = nullptr;
   if (x.splits > 1) {
-    pl = reinterpret_cast<float*>(ws);
-    po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 4, 256));
+    pl = reinterpret_cast<float2*>(ws);
+    po = reinterpret_cast<float*>(ws + align_up((size_t)x.splits * a.N * a.H * 8, 256));
   }
   const bool one = a.N <= (int64_t)a.S * x.tokens;
   const auto kernel = one ? cross_fwd_kernel<DH, true> : cross_fwd_kernel<DH, false>;
@@ -738,7 +774,7 @@ size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S)
   for (int r : {1, H / H_kv}) {
     if (r < 1 || r > 64 || (r & (r - 1))) continue;
     const int64_t splits = splits_of(N, L, H, r, S);
-    if (splits > 1) most = std::max(most, align_up((size_t)(splits * N * H * 4), 256) + (size_t)(splits * N * H * d_h * 4));
+    if (splits > 1) most = std::max(most, align_up((size_t)(splits * N * H * 8), 256) + (size_t)(splits * N * H * d_h * 4));
   }
   return most;
 }

@@ -526,3 +526,84 @@ def test_offsets_past_32_bits():
     k.copy_(c.k)
     c.in_place[1] = k
     check_backward(c, *check_forward(c))
+
+
+# ----------------------------------------------------------------------------- scores far from ordinary ones
+LOWEST = torch.finfo(torch.bfloat16).min
+HIDDEN = [float("-inf"), LOWEST, -3e30, -1e30, -1e12]
+
+
+class Masked(Case):
+    """A case behind `hidden` keys that a channel masks: q holds 1 there, those
+    keys `mask` and the others 0.  exp of their scores is 0 in 64 bits too
+    (each is below -8e10), so that results are those of the keys behind."""
+
+    def __init__(self, N, L, H, Hk, d, hidden, mask):
+        super().__init__([N], [L], H, Hk, d, seed=hidden)
+        self.q[..., 0], self.k[..., 0] = 1, 0
+        g = torch.Generator(device="cuda")
+        g.manual_seed(1)
+        k, v = (rnd(g, hidden, Hk, d).to(torch.bfloat16) for _ in range(2))
+        k[..., 0] = mask
+        self.in_place = [self.q, torch.cat([k, self.k]), torch.cat([v, self.v])]
+
+
+# one query tile and two, a whole hidden tile before the first key that counts, and part of one; in one range
+# of keys (few keys, or enough heads) and in shares, with whole shares hidden
+MASKED = [(60, 72, 2, 2, 128), (60, 40, 2, 1, 256 - 40), (200, 72, 2, 2, 128), (200, 300, 80, 80, 140),
+          (60, 300, 80, 80, 256), (5, 2000, 2, 2, 1300), (200, 2000, 4, 2, 700)]
+
+
+@pytest.mark.parametrize("mask", HIDDEN)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L,H,Hk,hidden", MASKED)
+def test_hidden_first_tiles(N, L, H, Hk, hidden, d, mask):
+    """Every score of a row's first key tiles is -inf or hugely negative, those behind are ordinary."""
+    c = Masked(N, L, H, Hk, d, hidden, mask)
+    r = c.reference()
+    out, lse = moga.cross_attn(*c.in_place, return_lse=True)
+    near(out, r["out"], B * np.abs(r["out"]) + (B + 2.0 ** -12 + 2 * c.delta) * r["out_size"], what="out")
+    near(lse, r["lse"], c.delta + 2.0 ** -16 + 2.0 ** -22 * np.abs(r["lse"]), what="lse")
+
+
+HUGE = [LOWEST / 4, -1e30, -1e12, -3e9, 3e9, 1e12, 1e30, -LOWEST / 4]
+
+
+@pytest.mark.parametrize("value", HUGE)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L", [(3, 1), (60, 77), (200, 130), (5, 3000), (200, 3000)])
+def test_keys_that_are_all_huge(N, L, d, value):
+    """All keys the same huge one: the mean of V.  All but one: that one's V, where it is larger.
+
+    P is exactly 1 or exactly 0 in both (the scores differ by over 2^20), so
+    out is rounded once, behind sums and a division in fp32 (2^-12)."""
+    c = Case([N], [L], 2, 2, d, seed=L)
+    one = torch.zeros(d, dtype=torch.bfloat16, device="cuda")
+    one[0] = 1
+    c.q[:], c.k[:] = one, value * one
+    v = around.f64(c.v)
+    for _ in range(2):
+        out, lse = moga.cross_attn(c.q, c.k, c.v, return_lse=True)
+        s = around.f64(c.k)[:, :, 0] / np.sqrt(d)                     # [L, H]
+        top = s == s.max(0)
+        for h in range(2):
+            w = v[top[:, h], h]
+            want, size = w.mean(0)[None].repeat(N, 0), np.abs(w).mean(0)[None]
+            near(out[:, h], want, B * np.abs(want) + 2.0 ** -12 * size, what="out")
+            want = np.full(N, s[:, h].max() + np.log(top[:, h].sum()))
+            near(lse[h], want, 2.0 ** -21 * np.abs(want), what="lse")
+        c.k[L // 2, :, 0] = 0.75 * value if value < 0 else 1.25 * value
+
+
+@pytest.mark.parametrize("N,L", [(3, 1), (60, 77), (200, 130), (5, 3000)])
+def test_rows_whose_scores_are_all_minus_infinity(N, L):
+    """As rows without keys: 0, and -inf.  Other rows of the tile are as ever."""
+    c = Case([N], [L], 2, 2, 64, seed=L)
+    c.q[..., 0], c.k[..., 0] = 0.25, float("-inf")
+    out, lse = moga.cross_attn(c.q, c.k, c.v, return_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+    c.k[:, 1, 0] = 0                                                  # the second head's keys count again
+    out, lse = moga.cross_attn(c.q, c.k, c.v, return_lse=True)
+    assert (out[:, 0] == 0).all() and torch.isneginf(lse[0]).all()
+    alone = moga.cross_attn(c.q[:, 1:].contiguous(), c.k[:, 1:].contiguous(), c.v[:, 1:].contiguous())
+    assert torch.isfinite(lse[1]).all() and (L > 1000 or torch.equal(out[:, 1:], alone))
