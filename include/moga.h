@@ -456,6 +456,9 @@ moga_status moga_cross_attn(const void* q, int64_t q_stride_n, int64_t q_stride_
  *      segment are left as they were (fill = 0) or get dq = 0 (fill = 1); key
  *      rows of no segment, or past its length, are left as they were.  All
  *      sums are taken in a fixed order.
+ * P = exp(S - lse) is formed anew from lse, which is fp32: it is right to about
+ * |lse| 2^-22.  A row whose |lse| is 2^20 or more, or -inf, gets dq = 0 and adds
+ * nothing to dk and dv.
  * dout, out, dq, dk, dv and ws are 32-byte aligned (whole sectors are read and
  * written).
  * Workspace: moga_cross_attn_backward_workspace_size(...) bytes. */

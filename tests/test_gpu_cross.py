@@ -607,3 +607,70 @@ def test_rows_whose_scores_are_all_minus_infinity(N, L):
     assert (out[:, 0] == 0).all() and torch.isneginf(lse[0]).all()
     alone = moga.cross_attn(c.q[:, 1:].contiguous(), c.k[:, 1:].contiguous(), c.v[:, 1:].contiguous())
     assert torch.isfinite(lse[1]).all() and (L > 1000 or torch.equal(out[:, 1:], alone))
+
+
+@pytest.mark.parametrize("mask", HIDDEN[1:])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L,H,Hk,hidden", MASKED)
+def test_gradients_behind_hidden_keys(N, L, H, Hk, hidden, d, mask):
+    """Hidden keys get gradients of 0 and change no others (those of -inf make dS K's channel 0 * inf, as the formula has it)."""
+    c = Masked(N, L, H, Hk, d, hidden, mask)
+    r = c.reference(c.dout)
+    out, lse = moga.cross_attn(*c.in_place, return_lse=True)
+    g = moga.cross_attn_backward(c.dout, *c.in_place, out, lse)
+    moga.sync_status(g["ws"])
+    assert (g["dk"][:hidden] == 0).all() and (g["dv"][:hidden] == 0).all()
+    g = dict(dq=g["dq"], dk=g["dk"][hidden:], dv=g["dv"][hidden:])
+    for n in ("dq", "dk"):
+        near(g[n], r[n], B * np.abs(r[n]) + (B + 2.0 ** -11) * r[n + "_size"] + B * r[n + "_d"] +
+             (2 * c.delta + 2.0 ** -14) * r[n + "_p"] + 2 * c.eta * r[n + "_1"], what=n)
+    near(g["dv"], r["dv"], B * np.abs(r["dv"]) + (B + 2.0 ** -11 + 2 * c.delta) * r["dv_size"], what="dv")
+
+
+FAR = 2.0 ** 20
+
+
+@pytest.mark.parametrize("value", [LOWEST / 4, -1e12, 3e9, 1.5 * FAR * 16, -1.5 * FAR * 16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,L,H,Hk", [(60, 77, 2, 2), (200, 130, 2, 1), (5, 3000, 2, 2), (200, 700, 80, 80)])
+def test_rows_with_a_huge_log_sum_exp_add_nothing(N, L, H, Hk, d, value):
+    """Half of the rows meet a huge score in every key: lse is past 2^20, and P cannot be formed from it.
+
+    Their dq is 0, and dk, dv are those of the other rows.  channel 0 of dq and
+    dk, which the huge numbers multiply, is left out."""
+    c = Case([N], [L], H, Hk, d, seed=L)
+    c.q[..., 0], c.k[..., 0] = 0, value
+    c.q[1::2, :, 0] = 1
+    out, lse = moga.cross_attn(c.q, c.k, c.v, return_lse=True)
+    assert (lse[:, 1::2].abs() > FAR).all()
+    g = moga.cross_attn_backward(c.dout, c.q, c.k, c.v, out, lse)
+    moga.sync_status(g["ws"])
+    # In channel 0 the terms of a sum dS K are up to sum_j |dS_ij| |value|; sum_j |dS_ij| <= 2 max |dP| passes 8 here,
+    # and 8 |value| fp32's largest number at LOWEST / 4: that sum may be infinite.
+    assert (g["dq"][1::2] == 0).all() and all(torch.isfinite(g[n][..., 1:]).all() for n in ("dq", "dk", "dv"))
+    q, k, dout = c.q[::2].contiguous(), c.k.clone(), c.dout[::2].contiguous()
+    k[..., 0] = 0                                                     # q's channel 0 is 0 in these rows
+    c.q, c.k, c.seg = q, k, [(0, len(q), 0, L)]
+    r = c.reference(dout)
+    g["dq"] = g["dq"][::2]
+    for n in ("dq", "dk"):
+        tol = B * np.abs(r[n]) + (B + 2.0 ** -11) * r[n + "_size"] + B * r[n + "_d"] + \
+            (2 * c.delta + 2.0 ** -14) * r[n + "_p"] + 2 * c.eta * r[n + "_1"]
+        near(g[n][..., 1:], r[n][..., 1:], tol[..., 1:], what=n)
+    near(g["dv"], r["dv"], B * np.abs(r["dv"]) + (B + 2.0 ** -11 + 2 * c.delta) * r["dv_size"], what="dv")
+
+
+def test_gradients_of_rows_whose_scores_are_all_minus_infinity():
+    """As of rows without keys: none.  (k holds no -inf here: q does, and k a positive channel.)"""
+    for N, L in ((60, 77), (200, 130), (5, 3000)):
+        c = Case([N], [L], 2, 2, 64, seed=L)
+        c.k[..., 0] = 0.5
+        q = c.q.clone()
+        q[1::2, :, 0] = float("-inf")
+        out, lse = moga.cross_attn(q, c.k, c.v, return_lse=True)
+        assert torch.isneginf(lse[:, 1::2]).all() and (out[1::2] == 0).all()
+        g = moga.cross_attn_backward(c.dout, q, c.k, c.v, out, lse)
+        assert (g["dq"][1::2] == 0).all() and torch.isfinite(g["dq"]).all() and torch.isfinite(g["dv"]).all()
+        even = [t[::2].contiguous() for t in (c.q, c.dout)]
+        r = around.cross(even[0], c.k, c.v, [(0, len(even[0]), 0, L)], even[1])
+        near(g["dv"], r["dv"], B * np.abs(r["dv"]) + (B + 2.0 ** -10) * r["dv_size"], what="dv")
