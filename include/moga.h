@@ -395,6 +395,14 @@ moga_status moga_qk_norm_rope(const void* q, int64_t q_stride_n, int64_t q_strid
                               const int* axes, const int* grid, int64_t token0, const int32_t* pos, int halves,
                               void* q_out, void* k_out, void* ws, size_t ws_bytes, void* stream);
 
+/* moga_qk_norm_rope_ex: as moga_qk_norm_rope; with fill = 1 the rows of a token
+ * that is skipped are set to NaN, with fill = 0 left as they were. */
+moga_status moga_qk_norm_rope_ex(const void* q, int64_t q_stride_n, int64_t q_stride_h, const void* k,
+                                 int64_t k_stride_n, int64_t k_stride_h, moga_dtype dt, int64_t N, int H_q, int H_k,
+                                 int d_h, const float* w_q, const float* w_k, float eps, const float* table, int P,
+                                 const int* axes, const int* grid, int64_t token0, const int32_t* pos, int halves,
+                                 void* q_out, void* k_out, int fill, void* ws, size_t ws_bytes, void* stream);
+
 /* moga_rope_table: table fp32 [P, d_h/2, 2] of (cos, sin) of p * theta^(-i/n)
  * for the i-th of an axis's n pairs ((1, 0) for pairs that do not turn); the
  * angles are formed in 64 bits.  axes: HOST int[3], their sum at most d_h/2. */
@@ -413,6 +421,17 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
                                        const float* w_k, float eps, const float* table, int P, const int* axes,
                                        const int* grid, int64_t token0, const int32_t* pos, int halves, void* dq,
                                        void* dk, float* dw_q, float* dw_k, void* ws, size_t ws_bytes, void* stream);
+
+/* moga_qk_norm_rope_backward_ex: as moga_qk_norm_rope_backward; with fill = 1
+ * dq and dk of a token that is skipped are set to NaN, with fill = 0 left as
+ * they were.  Either way it adds nothing to dw_q and dw_k. */
+moga_status moga_qk_norm_rope_backward_ex(const void* dq_out, const void* dk_out, const void* q, int64_t q_stride_n,
+                                          int64_t q_stride_h, const void* k, int64_t k_stride_n, int64_t k_stride_h,
+                                          moga_dtype dt, int64_t N, int H_q, int H_k, int d_h, const float* w_q,
+                                          const float* w_k, float eps, const float* table, int P, const int* axes,
+                                          const int* grid, int64_t token0, const int32_t* pos, int halves, void* dq,
+                                          void* dk, float* dw_q, float* dw_k, int fill, void* ws, size_t ws_bytes,
+                                          void* stream);
 
 /* ---------------------------------------------------------------- cross attention
  * moga_cross_attn: attention of N query tokens to L rows of an encoder's

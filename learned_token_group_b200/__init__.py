@@ -104,9 +104,13 @@ def get_lib():
         "moga_qk_norm_rope_workspace_size": (_SZ, []),
         "moga_qk_norm_rope": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P,
                                    _I64, _P, _I, _P, _P, _P, _SZ, _P]),
+        "moga_qk_norm_rope_ex": (_I, [_P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P,
+                                      _I64, _P, _I, _P, _P, _I, _P, _SZ, _P]),
         "moga_qk_norm_rope_backward_workspace_size": (_SZ, [_I]),
         "moga_qk_norm_rope_backward": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F,
                                             _P, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+        "moga_qk_norm_rope_backward_ex": (_I, [_P, _P, _P, _I64, _I64, _P, _I64, _I64, _I, _I64, _I, _I, _I, _P, _P, _F,
+                                               _P, _I, _P, _P, _I64, _P, _I, _P, _P, _P, _P, _I, _P, _SZ, _P]),
         "moga_cross_attn_workspace_size": (_SZ, [_I64, _I64, _I, _I, _I, _I]),
         "moga_cross_attn": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _I, _P, _P, _P,
                                  _I, _P, _P, _I, _P, _SZ, _P]),
@@ -669,8 +673,10 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], w_q: Opti
     axes and a grid (T, Hg, Wg), token0 being the first token's place on it, or
     with positions int32 [N, 3]; without a table the norm alone.  Returns
     (q_out, k_out), bf16 and dense, None for a side that was None; out: such a
-    pair to write to.  ws (``workspace``): for positions outside the table,
-    which ``sync_status`` reports; it is made when positions are given without it."""
+    pair to write to.  A token whose position is outside the table is skipped:
+    its rows are NaN in outputs made here, and left as they were in a given
+    ``out``.  ws (``workspace``): ``sync_status(ws)`` reports such tokens;
+    without it nothing does."""
     dev, _, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
     if out is None:
         q_out = None if q is None else _like(q, torch.bfloat16)
@@ -681,7 +687,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], w_q: Opti
     if ws is None and positions is not None:
         ws = workspace(256, dev)
     _device(ws, "ws", dev)
-    _call(dev, "moga_qk_norm_rope", *args, _at(q_out), _at(k_out), _at(ws), 0 if ws is None else ws.numel())
+    _call(dev, "moga_qk_norm_rope_ex", *args, _at(q_out), _at(k_out), int(out is None), _at(ws),
+          0 if ws is None else ws.numel())
     return q_out, k_out
 
 
@@ -694,7 +701,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     """Gradients of ``qk_norm_rope`` (moga_qk_norm_rope_backward in moga.h):
     dict(dq, dk, dw_q, dw_k, ws) from the gradients of its outputs (bf16,
     dense).  dq and dk have the inputs' type; dw_q, dw_k are fp32 [d_h], None
-    for a weight that is None.  Pass the ws back to reuse it."""
+    for a weight that is None.  A token that the forward skips gets NaN in dq
+    and dk and adds nothing to dw; ``sync_status(ws)`` reports it.  Pass the ws
+    back to reuse it."""
     dev, d_h, args = _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
     g = {"dq": None, "dk": None, "dw_q": None, "dw_k": None}
     for n, d, x, w in (("q", dq_out, q, w_q), ("k", dk_out, k, w_k)):
@@ -710,9 +719,9 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
     if ws is None or ws.numel() < need:
         ws = workspace(need, dev)
     _device(ws, "ws", dev)
-    _call(dev, "moga_qk_norm_rope_backward", None if q is None else dq_out.data_ptr(),
+    _call(dev, "moga_qk_norm_rope_backward_ex", None if q is None else dq_out.data_ptr(),
           None if k is None else dk_out.data_ptr(), *args, _at(g["dq"]), _at(g["dk"]), _at(g["dw_q"]), _at(g["dw_k"]),
-          ws.data_ptr(), ws.numel())
+          1, ws.data_ptr(), ws.numel())
     g["ws"] = ws
     return g
 

@@ -1224,17 +1224,29 @@ moga_status moga_qk_norm_rope(const void* q, int64_t q_sn, int64_t q_sh, const v
                               float eps, const float* table, int P, const int* axes, const int* grid, int64_t token0,
                               const int32_t* pos, int halves, void* q_out, void* k_out, void* ws, size_t ws_bytes,
                               void* stream) {
+  return moga_qk_norm_rope_ex(q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps, table, P, axes, grid,
+                              token0, pos, halves, q_out, k_out, 0, ws, ws_bytes, stream);
+}
+
+moga_status moga_qk_norm_rope_ex(const void* q, int64_t q_sn, int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh,
+                                 moga_dtype dt, int64_t N, int H_q, int H_k, int d_h, const float* w_q,
+                                 const float* w_k, float eps, const float* table, int P, const int* axes,
+                                 const int* grid, int64_t token0, const int32_t* pos, int halves, void* q_out,
+                                 void* k_out, int fill, void* ws, size_t ws_bytes, void* stream) {
   NormArgs a{};
   const moga_status st = norm_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps, table, P,
                                    axes, grid, token0, pos, halves);
   if (st != MOGA_OK) return st;
   if (N > 0 && ((H_q && !q_out) || (H_k && !k_out))) return MOGA_ERR_INVALID_ARG;
-  if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(ws) || (pos && !ws)) return MOGA_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(ws) || (pos && !ws) || fill < 0 ||
+      fill > 1)
+    return MOGA_ERR_INVALID_ARG;
   if (ws && ws_bytes < kHeader) return MOGA_ERR_WORKSPACE;
   DevCtx c;
   if (!make_ctx(&c, ws, stream)) return MOGA_ERR_CUDA;
   a.y[0] = q_out;
   a.y[1] = k_out;
+  a.fill = fill;
   int launches = 0;
   const cudaError_t e = launch_norm_rope(c, a, d_h, dt == MOGA_BF16, halves == 1, false, nullptr, nullptr, &launches);
   count((uint64_t)launches);
@@ -1251,13 +1263,24 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
                                        float eps, const float* table, int P, const int* axes, const int* grid,
                                        int64_t token0, const int32_t* pos, int halves, void* dq, void* dk,
                                        float* dw_q, float* dw_k, void* ws, size_t ws_bytes, void* stream) {
+  return moga_qk_norm_rope_backward_ex(dq_out, dk_out, q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps,
+                                       table, P, axes, grid, token0, pos, halves, dq, dk, dw_q, dw_k, 0, ws, ws_bytes,
+                                       stream);
+}
+
+moga_status moga_qk_norm_rope_backward_ex(const void* dq_out, const void* dk_out, const void* q, int64_t q_sn,
+                                          int64_t q_sh, const void* k, int64_t k_sn, int64_t k_sh, moga_dtype dt,
+                                          int64_t N, int H_q, int H_k, int d_h, const float* w_q, const float* w_k,
+                                          float eps, const float* table, int P, const int* axes, const int* grid,
+                                          int64_t token0, const int32_t* pos, int halves, void* dq, void* dk,
+                                          float* dw_q, float* dw_k, int fill, void* ws, size_t ws_bytes, void* stream) {
   NormArgs a{};
   const moga_status st = norm_args(&a, q, q_sn, q_sh, k, k_sn, k_sh, dt, N, H_q, H_k, d_h, w_q, w_k, eps, table, P,
                                    axes, grid, token0, pos, halves);
   if (st != MOGA_OK) return st;
   if (N > 0 && ((H_q && (!dq_out || !dq)) || (H_k && (!dk_out || !dk)))) return MOGA_ERR_INVALID_ARG;
   if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) || !aligned4(dw_q) ||
-      !aligned4(dw_k) || !ws || !aligned16(ws))
+      !aligned4(dw_k) || !ws || !aligned16(ws) || fill < 0 || fill > 1)
     return MOGA_ERR_INVALID_ARG;
   if (ws_bytes < moga_qk_norm_rope_backward_workspace_size(d_h)) return MOGA_ERR_WORKSPACE;
   DevCtx c;
@@ -1266,6 +1289,7 @@ moga_status moga_qk_norm_rope_backward(const void* dq_out, const void* dk_out, c
   a.dy[1] = dk_out;
   a.y[0] = dq;
   a.y[1] = dk;
+  a.fill = fill;
   a.part = reinterpret_cast<float*>((uint8_t*)ws + kHeader);
   int launches = 0;
   const cudaError_t e = launch_norm_rope(c, a, d_h, dt == MOGA_BF16, halves == 1, true, dw_q, dw_k, &launches);

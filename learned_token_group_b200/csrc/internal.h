@@ -169,6 +169,7 @@ struct NormArgs {
   int P, half, end0, end1, end2;
   const int32_t* pos;    // [N][3], or null: the place of token (token0 + n) mod cells on the grid
   uint32_t token0, cells, frame, width;
+  int fill;              // a token outside the table: rows of NaN; otherwise left as they were
   int chunks[2], rows[2];  // set by the launcher
 };
 cudaError_t launch_rope_table(const DevCtx& c, int P, int d_h, const int* axes, double theta, float* table);

@@ -188,6 +188,16 @@ __device__ __forceinline__ float dot8(const Eight& a, const Eight& b) {
   return x + y;
 }
 
+// NaN in a lane group's rows (h0, h0 + step, ...) of a token that is skipped.
+template <int DH, bool kHalves, typename T>
+__device__ __forceinline__ void fill_nan(const NormArgs& a, int64_t n, int t, int l, int h0, int step) {
+  const float x = __int_as_float(0x7fc00000);
+  const float v[8] = {x, x, x, x, x, x, x, x};
+  T* y = static_cast<T*>(a.y[t]) + n * a.heads[t] * DH;
+#pragma unroll 1
+  for (int u = 0, h = h0; u < a.rows[t] && h < a.heads[t]; ++u, h += step) store8<DH, kHalves>(y + h * DH, l, v);
+}
+
 // Sum over the lanes that share a row.
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
@@ -236,7 +246,10 @@ __global__ void __launch_bounds__(kNormThreads, 4) norm_rope_kernel(const NormAr
       if (u < a.rows[t] && h < a.heads[t]) load8<DH, kHalves>(raw[u], x + h * a.sh[t], l);
     }
     float c[4], s[4];
-    if (!angles<kRot>(a, it.n, l, c, s, status)) continue;
+    if (!angles<kRot>(a, it.n, l, c, s, status)) {
+      if (a.fill) fill_nan<DH, kHalves, __nv_bfloat16>(a, it.n, t, l, h0, RPW);
+      continue;
+    }
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;
@@ -288,7 +301,10 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_rope_bwd_kernel(const No
       }
     }
     float c[4], s[4];
-    if (!angles<kRot>(a, it.n, l, c, s, status)) continue;
+    if (!angles<kRot>(a, it.n, l, c, s, status)) {
+      if (a.fill) fill_nan<DH, kHalves, T>(a, it.n, t, l, h0, RPW);
+      continue;
+    }
     float w[8], dw[8] = {};
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = a.w[t] ? __ldg(a.w[t] + channel<DH, kHalves>(l, e)) : 1.0f;

@@ -203,3 +203,16 @@ def test_binding_refuses_host_tensors():
         moga.qk_norm_rope(None, None)
     with pytest.raises(ValueError, match="positions"):
         moga.rope_table(0, 64, (1, 1, 1), device="cuda:0")
+
+
+def test_fill_refusals(lib):
+    """fill of the _ex calls is 0 or 1."""
+    def f(fill):
+        return lib.moga_qk_norm_rope_ex(P, 256, 128, P, 256, 128, 1, 10, 2, 2, 128, None, None, 1e-6, None, 0, None, None,
+                                        0, None, 0, P, P, fill, None, 0, None)
+
+    def b(fill):
+        return lib.moga_qk_norm_rope_backward_ex(P, P, P, 256, 128, P, 256, 128, 1, 10, 2, 2, 128, None, None, 1e-6, None, 0,
+                                                 None, None, 0, None, 0, P, P, P, P, fill, P, BIG, None)
+    for fill in (-1, 2):
+        assert f(fill) == b(fill) == INVALID

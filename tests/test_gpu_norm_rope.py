@@ -382,3 +382,33 @@ def test_offsets_past_32_bits():
     got, _ = moga.qk_norm_rope(q, None)
     want, size = around.norm_rope(q, None, EPS, None, False)
     near(got, want, size, FWD, HALF[torch.bfloat16])
+
+
+def _used_memory(nbytes):
+    """Leaves the caching allocator blocks that hold ordinary numbers."""
+    for t in [torch.full((nbytes // 2,), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(4)]:
+        del t
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hk,d,halves", [(3, 2, 64, False), (1, 0, 128, True), (40, 40, 128, True), (17, 1, 64, False)])
+def test_skipped_tokens_are_nan_in_outputs_made_by_the_call(H, Hk, d, halves, dtype):
+    """What the memory held before never comes out as a result, from the calls or from autograd."""
+    a, ang = make(60, H, Hk, d, dtype, "dense", "list")
+    bad = [4, 5, 59]
+    a["positions"][4, 0], a["positions"][5, 1], a["positions"][59, 2] = -1, 64, 2 ** 31 - 1
+    keep = np.setdiff1d(np.arange(60), bad)
+    _used_memory(60 * H * d * 4)
+    dy = [None if a[n] is None else torch.ones(a[n].shape, dtype=torch.bfloat16, device="cuda") for n in "qk"]
+    out = moga.qk_norm_rope(**a, halves=halves)
+    g = moga.qk_norm_rope_backward(*dy, **a, halves=halves)
+    for n, y, t in zip("qk", out, dy):
+        if y is None:
+            continue
+        want, size = around.norm_rope(a[n], a["w_" + n], EPS, ang, halves)
+        assert torch.isnan(y[bad]).all()
+        near(y[keep], want[keep], size[keep], FWD, HALF[torch.bfloat16])
+        r = around.norm_rope_backward(np_cpu(t)[keep], np_cpu(a[n])[keep], a["w_" + n], EPS, ang[keep], halves)
+        assert torch.isnan(g["d" + n][bad]).all()
+        near(g["d" + n][keep], r["dx"], r["dx_size"], BWD, HALF[dtype])
+        near(g["dw_" + n], r["dw"], r["dw_size"], SUM, HALF[torch.float32])
