@@ -448,8 +448,9 @@ moga_status moga_qk_norm_rope_backward_ex(const void* dq_out, const void* dk_out
  *      q_offsets, kv_offsets device int32 [S+1], rising from 0 or more to at
  *      most N and L; NULL (only with S = 1): all rows.  kv_lens device int32
  *      [S], at most the distance to the next offset; NULL: all of it.
- *      Checked on the device: a violation skips all work and
- *      moga_sync_status() reports MOGA_ERR_DEVICE_CHECK.
+ *      Checked on the device: a violation skips all work (with fill = 1 out
+ *      and lse are set to NaN) and moga_sync_status() reports
+ *      MOGA_ERR_DEVICE_CHECK.
  * Out: out bf16 [N, H, d_h], dense, apart from the inputs; lse fp32 [H, N] or NULL: the natural
  *      log-sum-exp of each query's scaled scores.  A query whose segment has
  *      no keys, or whose scores are all -inf, gets out = 0 and lse = -inf.
@@ -472,7 +473,8 @@ moga_status moga_cross_attn(const void* q, int64_t q_stride_n, int64_t q_stride_
  * [N, H, d_h], dense), the forward's inputs and its out and lse.
  * Out: dq bf16 [N, H, d_h], dk, dv bf16 [L, H_kv, d_h], dense; dk and dv are
  *      summed over the query heads that share a key head.  Query rows of no
- *      segment are left as they were (fill = 0) or get dq = 0 (fill = 1); key
+ *      segment are left as they were (fill = 0) or get dq = 0 (fill = 1; NaN
+ *      in all of dq where the segments are refused); key
  *      rows of no segment, or past its length, are left as they were.  All
  *      sums are taken in a fixed order.
  * P = exp(S - lse) is formed anew from lse, which is fp32: it is right to about

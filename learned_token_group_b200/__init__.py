@@ -805,7 +805,9 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: Opt
     Without offsets all queries attend to all keys.  Returns out [N, H, d_h],
     or (out, lse [H, N]) with return_lse.  Rows of no segment are zero (lse
     -inf) in an output made here, and left as they were (lse not written) in
-    a given ``out``."""
+    a given ``out``.  Offsets or lengths that do not fit skip all work: an
+    output made here is then NaN (lse too), a given one left as it was, and
+    ``sync_status(ws)`` reports it; without a ws nothing does."""
     dev, sizes, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
     fill = out is None
     if fill:
@@ -826,13 +828,15 @@ def cross_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
                         ws: Optional[torch.Tensor] = None):
     """Gradients of ``cross_attn`` (moga_cross_attn_backward in moga.h): dict(dq,
     dk, dv, ws), bf16 and dense, from dout and the forward's out and lse.  Rows
-    of no segment get zero.  Pass the ws back to reuse it."""
+    of no segment get zero.  Where the segments do not fit, dq is NaN, dk and
+    dv are 0, and ``sync_status(ws)`` reports it.  Pass the ws back to reuse it."""
     dev, sizes, args = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
     _dense(dout, "dout", q.shape, torch.bfloat16, dev)
     _dense(out, "out", q.shape, torch.bfloat16, dev)
     _dense(lse, "lse", (sizes[2], sizes[0]), torch.float32, dev)
     dq = _like(q)
-    make = torch.empty if kv_offsets is None and kv_lens is None else torch.zeros  # keys may have gaps
+    # keys may have gaps, and segments that do not fit leave all of them out
+    make = torch.empty if q_offsets is None and kv_offsets is None and kv_lens is None else torch.zeros
     dk, dv = make((2, *k.shape), dtype=torch.bfloat16, device=dev)
     need = get_lib().moga_cross_attn_backward_workspace_size(*sizes)
     if ws is None or ws.numel() < need:

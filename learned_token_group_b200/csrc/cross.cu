@@ -140,7 +140,10 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
   float2* stat = reinterpret_cast<float2*>(smem + P::kStat);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (!segments_ok(a, status)) return;
+  if (!segments_ok(a, status)) {
+    if (a.fill) refuse_rows(a.out, a.lse, a.N * a.H, DH / 8);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);

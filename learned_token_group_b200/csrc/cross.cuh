@@ -308,6 +308,16 @@ __device__ __forceinline__ void fill_rows(const CrossArgs& a, void* out, float* 
   }
 }
 
+// Refused segments: NaN in every row of an output that is to be filled.  All
+// threads of the grid; out of line, since what a small call fetches counts.
+__device__ __noinline__ void refuse_rows(void* out, float* lse, int64_t rows, int pieces) {
+  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+  const uint32_t nan2 = 0x7fc07fc0u;  // two bf16 NaN
+  for (int64_t i = first; i < rows * pieces; i += step) static_cast<uint4*>(out)[i] = make_uint4(nan2, nan2, nan2, nan2);
+  if (lse)
+    for (int64_t i = first; i < rows; i += step) lse[i] = __int_as_float(0x7fc00000);
+}
+
 // The rows of segments without keys: 0, and lse = -inf where it is given.
 // One warp of `warps` in the grid.
 template <int DH>

@@ -166,7 +166,10 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
                 unsigned long long wait_ns) {
   using P = BPlan<DH>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (!base_ok(smem, status) || !segments_ok(a, status)) return;
+  if (!base_ok(smem, status) || !segments_ok(a, status)) {
+    if (a.fill) refuse_rows(a.dq, nullptr, a.N * a.H, DH / 8);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + P::kBar);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;

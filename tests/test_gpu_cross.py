@@ -674,3 +674,32 @@ def test_gradients_of_rows_whose_scores_are_all_minus_infinity():
         even = [t[::2].contiguous() for t in (c.q, c.dout)]
         r = around.cross(even[0], c.k, c.v, [(0, len(even[0]), 0, L)], even[1])
         near(g["dv"], r["dv"], B * np.abs(r["dv"]) + (B + 2.0 ** -10) * r["dv_size"], what="dv")
+
+
+@pytest.mark.parametrize("bad", BAD + [dict(q_offsets=[0, 101], one=True), dict(kv_lens=[81], one=True),
+                                       dict(kv_offsets=[5, 3], one=True)], ids=str)
+def test_refused_segments_leave_nan_in_outputs_made_by_the_call(bad):
+    """What the memory held before never comes out as a result: out, lse and dq are NaN, dk and dv 0."""
+    bad = dict(bad)
+    seg = {} if bad.pop("one", False) else dict(q_offsets=[0, 50, 100], kv_offsets=[0, 40, 80], kv_lens=[40, 40])
+    c = Case([100], [80], 2, 2, 64)
+    good = {n: ints(x) for n, x in seg.items()}
+    broken = {n: ints(x) for n, x in dict(seg, **bad).items()}
+    for n in (1, 3):                                  # one range of keys for a CTA, and shares (3 x 2,000 keys)
+        q, k, v, dout = c.q, c.k, c.v, c.dout
+        if n == 3:
+            if seg or "kv_lens" not in bad:
+                break
+            c = Case([3], [2000], 2, 2, 64)
+            q, k, v, dout, broken = c.q, c.k, c.v, c.dout, dict(kv_lens=ints([2001]))
+        out0, lse0 = moga.cross_attn(q, k, v, **(good if n == 1 else {}), return_lse=True)
+        for t in [torch.full((200 * 2 * 64,), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(8)] + \
+                 [torch.full_like(lse0, 5.0) for _ in range(8)]:
+            del t
+        out, lse = moga.cross_attn(q, k, v, **broken, return_lse=True)
+        assert torch.isnan(out).all() and torch.isnan(lse).all()
+        assert torch.isnan(moga.cross_attn(q, k, v, **broken)).all()
+        g = moga.cross_attn_backward(dout, q, k, v, out0, lse0, **broken)
+        assert torch.isnan(g["dq"]).all() and (g["dk"] == 0).all() and (g["dv"] == 0).all()
+        with pytest.raises(moga.MogaError):
+            moga.sync_status(g["ws"])
