@@ -22,8 +22,8 @@ import torch
 __all__ = ["MogaError", "get_lib", "LIB_PATH", "HEADER_PATH", "route", "group_attn", "stga_window_attn",
            "moga_layer", "sync_status", "workspace", "MogaLayer", "exported_names", "kernel_launches",
            "set_timing_events", "STAGES", "Pipeline", "stga_shot_attn", "moga_layer_shots", "sort",
-           "layer_train", "layer_backward", "MogaFunction", "rope_table", "qk_norm_rope", "qk_norm_rope_backward",
-           "QkNormRopeFunction", "cross_attn_workspace_size", "cross_attn", "cross_attn_backward",
+           "layer_train", "layer_backward", "MogaFunction", "rope_table", "qk_norm_rope_workspace_size", "qk_norm_rope",
+           "qk_norm_rope_backward", "QkNormRopeFunction", "cross_attn_workspace_size", "cross_attn", "cross_attn_backward",
            "CrossAttnFunction"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -613,6 +613,19 @@ def rope_table(P: int, d_h: int, axes: Sequence[int], theta: float = 10000.0, de
     return table
 
 
+def _enough(ws: Optional[torch.Tensor], need: int):
+    """Refuses a ws that the backward pass would have to replace: its status would be lost."""
+    if ws is not None and ws.numel() < need:
+        raise ValueError(f"ws must hold {need} bytes for both passes, got {ws.numel()}")
+
+
+def qk_norm_rope_workspace_size(d_h: int, backward: bool = False) -> int:
+    """Bytes of a workspace that ``qk_norm_rope`` (and, with backward, ``qk_norm_rope_backward``) takes."""
+    lib = get_lib()
+    n = lib.moga_qk_norm_rope_workspace_size()
+    return max(n, lib.moga_qk_norm_rope_backward_workspace_size(int(d_h))) if backward else n
+
+
 def _norm_setup(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves):
     """Checks the shared arguments: (device, d_h, the C call's arguments from q on)."""
     x = k if q is None else q
@@ -729,16 +742,22 @@ def qk_norm_rope_backward(dq_out: Optional[torch.Tensor], dk_out: Optional[torch
 class QkNormRopeFunction(torch.autograd.Function):
     """``qk_norm_rope`` under torch.autograd: q_out, k_out =
     QkNormRopeFunction.apply(q, k, w_q, w_k, table, axes, grid, positions,
-    token0, eps, halves).  q, k, w_q, w_k get gradients.  q and k may be views;
-    those the kernels cannot read in place are copied."""
+    token0, eps, halves, ws).  q, k, w_q, w_k get gradients.  q and k may be
+    views; those the kernels cannot read in place are copied.  ws: a workspace
+    of ``qk_norm_rope_workspace_size(d_h, backward=True)`` bytes for both
+    passes, where ``sync_status(ws)`` reports tokens outside the table; without
+    one they are NaN and nothing reports them."""
 
     @staticmethod
     def forward(ctx, q, k, w_q=None, w_k=None, table=None, axes=None, grid=None, positions=None, token0=0, eps=1e-6,
-                halves=False):
+                halves=False, ws=None):
         q, k = _readable(q), _readable(k)
+        x = k if q is None else q
+        if x is not None:
+            _enough(ws, qk_norm_rope_workspace_size(x.shape[-1], backward=True))
         ctx.save_for_backward(q, k, w_q, w_k, table, positions)
-        ctx.args = (axes, grid, token0, eps, halves)
-        return qk_norm_rope(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves)
+        ctx.args, ctx.ws = (axes, grid, token0, eps, halves), ws
+        return qk_norm_rope(q, k, w_q, w_k, table, axes, grid, positions, token0, eps, halves, ws=ws)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -749,8 +768,8 @@ class QkNormRopeFunction(torch.autograd.Function):
             torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device) if d is None
             else d.to(torch.bfloat16).contiguous())
         g = qk_norm_rope_backward(full(dq_out, q), full(dk_out, k), q, k, w_q, w_k, table, axes, grid, positions,
-                                  token0, eps, halves)
-        return g["dq"], g["dk"], g["dw_q"], g["dw_k"], None, None, None, None, None, None, None
+                                  token0, eps, halves, ws=ctx.ws)
+        return g["dq"], g["dk"], g["dw_q"], g["dw_k"], None, None, None, None, None, None, None, None
 
 
 def _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens):
@@ -849,16 +868,23 @@ def cross_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v:
 
 class CrossAttnFunction(torch.autograd.Function):
     """``cross_attn`` under torch.autograd: out = CrossAttnFunction.apply(q, k,
-    v, q_offsets, kv_offsets, kv_lens); q, k and v get gradients.  The inputs
-    may be views; those the kernels cannot read in place are copied.  To put a
-    training step into a CUDA graph, capture ``cross_attn`` and
-    ``cross_attn_backward`` themselves."""
+    v, q_offsets, kv_offsets, kv_lens, ws); q, k and v get gradients.  The
+    inputs may be views; those the kernels cannot read in place are copied.
+    ws: a workspace of ``cross_attn_workspace_size(q, k, segments,
+    backward=True)`` bytes for both passes, where ``sync_status(ws)`` reports
+    refused segments and waits that ran out; without one refused segments give
+    NaN and nothing reports either.  To put a training step into a CUDA graph,
+    capture ``cross_attn`` and ``cross_attn_backward`` themselves."""
 
     @staticmethod
-    def forward(ctx, q, k, v, q_offsets=None, kv_offsets=None, kv_lens=None):
+    def forward(ctx, q, k, v, q_offsets=None, kv_offsets=None, kv_lens=None, ws=None):
         q, k, v = (_readable(t, head_major=True) for t in (q, k, v))
-        out, lse = cross_attn(q, k, v, q_offsets, kv_offsets, kv_lens, return_lse=True)
+        if ws is not None:
+            S = max([1] + [t.numel() - 1 for t in (q_offsets, kv_offsets) if t is not None])
+            _enough(ws, cross_attn_workspace_size(q, k, S, backward=True))
+        out, lse = cross_attn(q, k, v, q_offsets, kv_offsets, kv_lens, return_lse=True, ws=ws)
         ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets, kv_lens)
+        ctx.ws = ws
         return out
 
     @staticmethod
@@ -868,8 +894,8 @@ class CrossAttnFunction(torch.autograd.Function):
         dout = dout.to(torch.bfloat16).contiguous()
         if dout.data_ptr() % 32:
             dout = dout.clone()
-        g = cross_attn_backward(dout, q, k, v, out, lse, *seg)
-        return g["dq"], g["dk"], g["dv"], None, None, None
+        g = cross_attn_backward(dout, q, k, v, out, lse, *seg, ws=ctx.ws)
+        return g["dq"], g["dk"], g["dv"], None, None, None, None
 
 
 def _host_tensor(t: torch.Tensor, name: str, dtype, shape):

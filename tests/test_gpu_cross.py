@@ -703,3 +703,56 @@ def test_refused_segments_leave_nan_in_outputs_made_by_the_call(bad):
         assert torch.isnan(g["dq"]).all() and (g["dk"] == 0).all() and (g["dv"] == 0).all()
         with pytest.raises(moga.MogaError):
             moga.sync_status(g["ws"])
+
+
+def test_autograd_reports_to_a_given_workspace():
+    """Both passes of the function use the caller's ws: it reports what each refused, and is refused if too small."""
+    c = Case([50, 50], [40, 40], 2, 2, 64)
+    q, k, v = (t.clone().requires_grad_() for t in (c.q, c.k, c.v))
+    ws = moga.workspace(moga.cross_attn_workspace_size(q, k, 2, backward=True), "cuda")
+    qo, ko, kl = ints([0, 50, 100]), ints([0, 40, 80]), ints([40, 40])
+    out = moga.CrossAttnFunction.apply(q, k, v, qo, ko, kl, ws)
+    out.backward(c.dout)
+    moga.sync_status(ws)
+    good = [t.grad.clone() for t in (q, k, v)]
+    plain = moga.CrossAttnFunction.apply(q, k, v, qo, ko, kl)
+    assert torch.equal(plain, out)
+    kl[1] = 41
+    bad = moga.CrossAttnFunction.apply(q, k, v, qo, ko, kl, ws)
+    with pytest.raises(moga.MogaError) as e:
+        moga.sync_status(ws)
+    assert e.value.status == DEVICE_CHECK and torch.isnan(bad).all()
+    q.grad = k.grad = v.grad = None
+    bad.backward(c.dout)
+    with pytest.raises(moga.MogaError):
+        moga.sync_status(ws)
+    assert torch.isnan(q.grad).all() and (k.grad == 0).all() and (v.grad == 0).all()
+    kl[1] = 40
+    q.grad = k.grad = v.grad = None
+    moga.CrossAttnFunction.apply(q, k, v, qo, ko, kl, ws).backward(c.dout)
+    moga.sync_status(ws)
+    assert all(torch.equal(t.grad, x) for t, x in zip((q, k, v), good))
+    with pytest.raises(ValueError, match="ws"):
+        moga.CrossAttnFunction.apply(q, k, v, qo, ko, kl, ws[:256])
+
+
+def test_one_workspace_for_a_training_step():
+    """Norm and cross attention of a step, one after the other, with one ws of the largest size."""
+    c = Case([100], [80], 2, 2, 64)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    need = max(moga.cross_attn_workspace_size(c.q, c.k, backward=True), moga.qk_norm_rope_workspace_size(64, backward=True))
+
+    def step(ws):
+        q = c.q.clone().requires_grad_()
+        k = c.k.clone().requires_grad_()
+        w.grad = None
+        rest = (None, None, None, None, 0, 1e-6, False, ws)
+        a, _ = moga.QkNormRopeFunction.apply(q, None, w, None, *rest)
+        _, b = moga.QkNormRopeFunction.apply(None, k, None, w, *rest)
+        moga.CrossAttnFunction.apply(a, b, c.v, None, None, None, ws).backward(c.dout)
+        return q.grad, k.grad, w.grad.clone()
+    ws = moga.workspace(need, "cuda")
+    want = step(None)
+    for _ in range(2):
+        assert all(torch.equal(x, y) for x, y in zip(step(ws), want))
+    moga.sync_status(ws)

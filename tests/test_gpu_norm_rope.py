@@ -412,3 +412,29 @@ def test_skipped_tokens_are_nan_in_outputs_made_by_the_call(H, Hk, d, halves, dt
         assert torch.isnan(g["d" + n][bad]).all()
         near(g["d" + n][keep], r["dx"], r["dx_size"], BWD, HALF[dtype])
         near(g["dw_" + n], r["dw"], r["dw_size"], SUM, HALF[torch.float32])
+
+
+def test_autograd_reports_to_a_given_workspace():
+    """Both passes of the function use the caller's ws: it reports what each skipped, and is refused if too small."""
+    a, _ = make(60, 3, 2, 64, torch.bfloat16, "dense", "list")
+    a["q"].requires_grad_()
+    ws = moga.workspace(moga.qk_norm_rope_workspace_size(64, backward=True), "cuda")
+    args = [a[n] for n in ("q", "k", "w_q", "w_k", "table", "axes")] + [None, a["positions"], 0, EPS, False]
+    q, k = moga.QkNormRopeFunction.apply(*args, ws)
+    (q.float().sum() + k.float().sum()).backward()
+    moga.sync_status(ws)
+    good = a["q"].grad.clone()
+    a["positions"][7, 0] = 64
+    q, k = moga.QkNormRopeFunction.apply(*args, ws)
+    with pytest.raises(moga.MogaError) as e:
+        moga.sync_status(ws)
+    assert e.value.status == DEVICE_CHECK and torch.isnan(q[7]).all() and torch.isnan(k[7]).all()
+    a["q"].grad = None
+    torch.autograd.backward([q, k], [torch.ones_like(q), torch.ones_like(k)])
+    with pytest.raises(moga.MogaError):
+        moga.sync_status(ws)
+    keep = [n for n in range(60) if n != 7]
+    assert torch.isnan(a["q"].grad[7]).all() and torch.equal(a["q"].grad[keep], good[keep])
+    moga.sync_status(ws)
+    with pytest.raises(ValueError, match="ws"):
+        moga.QkNormRopeFunction.apply(*args, moga.workspace(256, "cuda"))
