@@ -764,9 +764,14 @@ class QkNormRopeFunction(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, w_q, w_k, table, positions = ctx.saved_tensors
         axes, grid, token0, eps, halves = ctx.args
-        full = lambda d, x: None if x is None else (  # noqa: E731
-            torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device) if d is None
-            else d.to(torch.bfloat16).contiguous())
+
+        def full(d, x):
+            if x is None:
+                return None
+            if d is None:
+                return torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
+            d = d.to(torch.bfloat16).contiguous()
+            return d.clone() if d.data_ptr() % 16 else d  # a slice of a flat buffer may start anywhere
         g = qk_norm_rope_backward(full(dq_out, q), full(dk_out, k), q, k, w_q, w_k, table, axes, grid, positions,
                                   token0, eps, halves, ws=ctx.ws)
         return g["dq"], g["dk"], g["dw_q"], g["dw_k"], None, None, None, None, None, None, None, None

@@ -438,3 +438,18 @@ def test_autograd_reports_to_a_given_workspace():
     moga.sync_status(ws)
     with pytest.raises(ValueError, match="ws"):
         moga.QkNormRopeFunction.apply(*args, moga.workspace(256, "cuda"))
+
+
+@pytest.mark.parametrize("first", [1, 3, 8])
+def test_autograd_takes_gradients_that_start_anywhere(first):
+    """An output's gradient may be a slice of a flat buffer, off a 16-byte boundary."""
+    a, _ = make(30, 2, 1, 64, torch.bfloat16, "dense", "grid")
+    a["q"].requires_grad_()
+    a["k"].requires_grad_()
+    args = [a[n] for n in ("q", "k", "w_q", "w_k", "table", "axes", "grid")] + [None, a["token0"]]
+    flat = torch.randn(30 * 3 * 64 + 16, device="cuda").to(torch.bfloat16)
+    dq = flat[first:first + 30 * 2 * 64].view(30, 2, 64)
+    dk = flat[first + 30 * 2 * 64:][:30 * 64].view(30, 1, 64)
+    got = torch.autograd.grad(moga.QkNormRopeFunction.apply(*args), [a["q"], a["k"]], [dq, dk])
+    want = torch.autograd.grad(moga.QkNormRopeFunction.apply(*args), [a["q"], a["k"]], [dq.clone(), dk.clone()])
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
