@@ -444,8 +444,11 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
     const float scale_log2 = 1.4426950408889634f * rsqrtf((float)DH);
     uint32_t sph = 0, un = 0;  // phases of s_full: bit by barrier
     uint32_t ones = 0;         // steps of units with one tile so far
+    // Tile B's warps pass over units without one, and then wait for as long as
+    // such a unit takes, for the next unit or for its first S.
+    const WaitCtx wx = x ? unit_wait(wc) : wc;
     bool ok = true;
-    while (ok && feed.next<true>(u, wc)) {
+    while (ok && feed.next<true>(u, wx)) {
       const int n = (u.k1 - u.k0 + kTile - 1) / kTile;
       const bool alone = u.q0 + xg.tokens >= u.q1, single = kOne && alone;  // tile A takes turns in both buffers
       if (n == 0 || (alone && x == 1)) continue;
@@ -456,7 +459,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         const int odd = single ? j & 1 : 0;
         const int buf = odd ? 2 : x;
         const uint32_t tSx = tS(x + odd) + lane_base;
-        if (!wait_for(&s_full[buf], (sph >> buf) & 1, wc)) { ok = false; break; }
+        if (!wait_for(&s_full[buf], (sph >> buf) & 1, wx)) { ok = false; break; }
         sph ^= 1u << buf;
         tc_fence_after();
         const int valid = u.k1 - u.k0 - j * kTile;

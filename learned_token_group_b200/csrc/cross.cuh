@@ -75,8 +75,8 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
   return mbar_try_wait(bar, parity) || wait_more<kSleep>(smem_u32(bar), parity, c);
 }
 
-// For waits that last as long as a unit does (the writers of its results, and
-// the walk, which is a unit ahead): the roles that step through the unit bound
+// For waits that last as long as a unit does (the writers of its results, the
+// walk, which is a unit ahead, and warps that a unit has no rows for): the roles that step through the unit bound
 // it, and their abort flag ends these too.
 __device__ __forceinline__ WaitCtx unit_wait(WaitCtx c) {
   c.limit_ns = c.limit_ns < (1ull << 33) ? c.limit_ns * 256 : c.limit_ns;

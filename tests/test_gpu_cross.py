@@ -756,3 +756,25 @@ def test_one_workspace_for_a_training_step():
     for _ in range(2):
         assert all(torch.equal(x, y) for x, y in zip(step(ws), want))
     moga.sync_status(ws)
+
+
+def test_a_unit_longer_than_the_wait_limit():
+    """Softmax warps without a tile of their own wait as long as a unit takes: that is no wait that ran out.
+
+    200 units of one query tile and 1,200,000 keys each (some 9,400 tiles, several
+    milliseconds) against a limit of 2 ms a step."""
+    lib = moga.get_lib()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    L = 1_200_000
+    q, k = rnd(g, 1, 200, 64).to(torch.bfloat16), rnd(g, L, 1, 64).to(torch.bfloat16)
+    ws = moga.workspace(moga.cross_attn_workspace_size(q, k), "cuda")
+    want = moga.cross_attn(q, k, k, ws=ws)
+    moga.sync_status(ws)
+    old = lib.moga_set_wait_limit_ns(2_000_000)
+    try:
+        got = moga.cross_attn(q, k, k, ws=ws)
+        moga.sync_status(ws)
+    finally:
+        lib.moga_set_wait_limit_ns(old)
+    assert torch.equal(got, want)
