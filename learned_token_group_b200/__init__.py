@@ -605,9 +605,11 @@ def rope_table(P: int, d_h: int, axes: Sequence[int], theta: float = 10000.0, de
 
     axes: how many pairs turn with the token's frame, row and column."""
     dev = torch.device(device)
-    dev = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
     if P < 1 or d_h not in (64, 128):
         raise ValueError(f"a table needs P >= 1 positions and d_h 64 or 128, got {P} and {d_h}")
+    if dev.type != "cuda":
+        raise ValueError(f"a table is made on a CUDA device, got {dev}")
+    dev = torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
     table = torch.empty((P, d_h // 2, 2), dtype=torch.float32, device=dev)
     _call(dev, "moga_rope_table", P, d_h, _triple(*map(int, axes)), float(theta), table.data_ptr())
     return table

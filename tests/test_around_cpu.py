@@ -216,3 +216,9 @@ def test_fill_refusals(lib):
                                                  None, None, 0, None, 0, P, P, P, P, fill, P, BIG, None)
     for fill in (-1, 2):
         assert f(fill) == b(fill) == INVALID
+
+
+def test_rope_table_refuses_a_host_device():
+    for dev in ("cpu", "meta"):
+        with pytest.raises(ValueError, match="CUDA"):
+            moga.rope_table(8, 64, (1, 1, 1), device=dev)
