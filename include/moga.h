@@ -161,7 +161,8 @@ moga_status moga_route_noalloc_status(void* stream);
  *              SA(q[perm[j],h], K_seg(j),h, V_seg(j),h)
  * where seg(j) is the segment of offsets that contains j.  gate may be NULL
  * (gate = 1).  Tokens of empty groups do not exist, so every token's row of
- * `out` is written exactly once.
+ * `out` is written exactly once.  Scores are fp32 of any size; a row whose
+ * scores are all -inf is 0 (here and in STGA).
  * In:  q, k, v bf16 [N, H, d_h]; perm int32 [N]; offsets int32 [M+1]
  *      (non-decreasing, offsets[0] = 0, offsets[M] = N); gate fp32 [N] or
  *      NULL.  The device checks offsets and every perm entry it uses: a
@@ -292,7 +293,9 @@ moga_status moga_layer_train(const void* x, const void* W_r, const float* b_r, m
  * The inputs (x, W_r, b_r, q, k, v, group_id, gate, perm, offsets, o_moga,
  * o_stga, lse_*) must be those of the forward call.  dW_r and db_r are
  * summed in a fixed order (deterministic); bf16 outputs are rounded once per
- * branch (the STGA share is added to the MoGA share in bf16).
+ * branch (the STGA share is added to the MoGA share in bf16).  P = exp(S - lse)
+ * is formed anew from the fp32 lse_*: a row whose |lse| is 2^20 or more, or
+ * -inf, adds nothing to dq, dk and dv.
  * Workspace: moga_layer_backward_workspace_size(N, d, H, d_h, M) bytes
  * (head-major copies of q, k, v and dO, plus per-token scratch). */
 size_t moga_layer_backward_workspace_size(int64_t N, int d, int H, int d_h, int M);

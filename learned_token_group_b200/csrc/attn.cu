@@ -686,7 +686,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         if (status) atomicOr(status, DEV_RANGE);
       }
       const int src = live ? (a.perm ? a.perm[u.start + r] : u.start + r) : 0;
-      float m_run = -INFINITY;
+      float m_run = kNoMax;
       uint64_t la = f2_pack(0.f, 0.f), lb = la, lc = la, ld = la;  // row sum of P, 8 partial sums
       for (int j = 0; j < nkv; ++j) {
         if (!mbar_wait(&s_full[x], sc & 1, wc, 6 + 16 * x, sc)) { ok = false; break; }
@@ -713,7 +713,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
           m8[i] = fmaxf(m, sr[16 * i + 15]);
         }
         const float mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
-        const float m_new = fmaxf(m_run, mx * scale_log2);
+        const float m_new = fmaxf(m_run, mx);
         // O_x was last written by the previous P V product, which completed
         // before this S (the MMA thread issued it first).  The running max is
         // moved (and O rescaled) only when it grows by more than 2^8; P and l
@@ -723,10 +723,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         if (j == 0) {
           m_run = m_new;
         } else {
-          const bool need = m_new > m_run + 8.0f;
+          const bool need = (m_new - m_run) * scale_log2 > 8.0f;
           rescale = __any_sync(0xffffffffu, need);
           if (need) {
-            alpha = fast_exp2(m_run - m_new);
+            alpha = P_moved(m_run, m_new, scale_log2);
             const uint64_t a2 = f2_pack(alpha, alpha);
             la = f2_mul(la, a2);
             lb = f2_mul(lb, a2);
@@ -738,8 +738,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         // P = 2^(S*scale - m), summed into l and written back over S as packed
         // bf16 (two keys per TMEM column); pairs of keys go through the packed
         // fp32x2 FMA/ADD units.  Masked keys are -inf, so their P is 0.
-        const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
-        const uint64_t nm2 = f2_pack(-m_run, -m_run);
+        uint64_t sc2, nm2;
+        P_factors(m_run, scale_log2, sc2, nm2);
 #pragma unroll
         for (int c = 0; c < kTile / 32; ++c) {
           uint32_t pk[16];
@@ -792,13 +792,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
       }
       float l_lo, l_hi;
       f2_unpack(f2_add(f2_add(la, lb), f2_add(lc, ld)), l_lo, l_hi);
-      // log-sum-exp of the scaled scores: S*scale = log2(e)^-1 (m + log2 l)
-      if (a.lse && live) a.lse[(int64_t)u.h * N + u.start + r] = (m_run + log2f(l_lo + l_hi)) * 0.6931471805599453f;
+      // A row whose scores are all -inf counts as one without keys: out 0, lse
+      // -inf.  Its l is 0 or a few 2^-126 (the polynomial's least); others' are
+      // 2^-16 at least.
+      float l = l_lo + l_hi;
+      const bool none = l < 1e-30f;
+      if (none) l = 0.0f;
+      if (a.lse && live) a.lse[(int64_t)u.h * N + u.start + r] = lse_of(l, m_run, scale_log2);
       const float gt = (live && a.gate) ? a.gate[src] : 1.0f;
       // output rows are written once: mark them first out of L2, so the K/V
       // tiles that other CTAs still read stay
       const uint64_t pol_out = l2_policy_evict_first();
-      const float inv = a.out_scale * gt / (l_lo + l_hi);
+      const float inv = none ? 0.0f : a.out_scale * gt / l;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(a.out) + ((int64_t)src * a.H + u.h) * (int64_t)DH;
 #pragma unroll
       for (int c = 0; c < DH / 32; ++c) {

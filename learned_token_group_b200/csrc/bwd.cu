@@ -251,7 +251,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tx1, const __grid_constant__
         const int pos = i * kYRows + lane + 32 * q;
         const bool valid = pos < u.len;
         const int64_t gi = (int64_t)u.h * N + u.start + pos;
-        lv[q] = valid ? -a.lse[gi] * kLog2e : -INFINITY;
+        lv[q] = valid ? neg_lse_log2(a.lse[gi]) : -INFINITY;
         dv[q] = valid ? a.dsum[gi] : 0.0f;
       }
     };
@@ -461,7 +461,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tx1, const __grid_constant__
       float nl_row = -INFINITY, d_row = 0.0f;  // dQ: this query row's -lse*log2(e) and D
       if (kDQ && live) {
         const int64_t gi = (int64_t)u.h * N + u.start + r;
-        nl_row = -a.lse[gi] * kLog2e;
+        nl_row = neg_lse_log2(a.lse[gi]);
         d_row = a.dsum[gi];
       }
       const int src = live ? (a.perm ? a.perm[u.start + r] : u.start + r) : 0;

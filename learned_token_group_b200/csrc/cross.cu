@@ -37,47 +37,22 @@
 // HBM and the epilogue with short ones.
 // With few units the key range is split over CTAs, which write O / l and (l, m)
 // in fp32, and cross_join_kernel joins them.
-//
-// P = exp2(S scale - fl(m scale)) in one fused step, m the running maximum of
-// the scores themselves.  The rounding of m scale is a factor of P that l shares;
-// but it passes 2^128 once m scale is past 2^32, and P would be infinite or 0.
-// Past kFar = 2^29 two scores that differ do so by |m| 2^-24 at least, 32 in the
-// exponent: the smaller one's weight is nothing in fp32, at half the scale too.
-// There the scale is a power of two, whose products are exact: P = 1 at the
-// maximum.  Only the row's two factors change; subtracting m from every S first
-// cost 1 to 4 %.  m starts at the lowest finite value, not at -inf: a tile of
-// scores of -inf gives P = 0, where -inf - -inf is NaN for all tiles behind it.
+// How P keeps clear of infinities at scores of any size: P_factors in ptx.cuh.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cfloat>
 
 #include "cross.cuh"
 
 namespace moga {
 namespace {
 
-constexpr float kFar = 536870912.0f;
-constexpr float kFarScale = 0.125f;  // the power of two below log2(e) / sqrt(64) and log2(e) / sqrt(128)
-
-// 2^((m - to) scale), to >= m: what a sum over P with m for reference takes for `to`.
-__device__ __forceinline__ float moved(float m, float to, float scale_log2) {
-  const float ms = m * scale_log2;
-  if (fabsf(ms) > kFar) return m == to ? 1.0f : 0.0f;
-  return fast_exp2(ms - to * scale_log2);
-}
-
 template <int C>
 __device__ __forceinline__ void store_row(void* base, int64_t at, int lane, const float (&x)[C], float f) {
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + at + lane * C;
 #pragma unroll
   for (int i = 0; i < C; ++i) p[i] = __float2bfloat16(x[i] * f);
-}
-
-// Natural log-sum-exp of the scaled scores from l and m; -inf for l = 0.
-__device__ __forceinline__ float lse_of(float l, float m, int d_h) {
-  return (m * (1.4426950408889634f * rsqrtf((float)d_h)) + log2f(l)) * 0.6931471805599453f;
 }
 
 template <int DH>
@@ -452,7 +427,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       const int n = (u.k1 - u.k0 + kTile - 1) / kTile;
       const bool alone = u.q0 + xg.tokens >= u.q1, single = kOne && alone;  // tile A takes turns in both buffers
       if (n == 0 || (alone && x == 1)) continue;
-      float m_run = -FLT_MAX;
+      float m_run = kNoMax;
       uint64_t l2 = f2_pack(0.f, 0.f);
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
@@ -511,15 +486,15 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
           const bool need = (m_new - m_run) * scale_log2 > 8.0f;
           rescale = __any_sync(0xffffffffu, need);
           if (need) {
-            alpha = moved(m_run, m_new, scale_log2);
+            alpha = P_moved(m_run, m_new, scale_log2);
             l2 = f2_mul(l2, f2_pack(alpha, alpha));
             m_run = m_new;
           }
         }
         // P = 2^(S scale - m scale) to bf16, the operand's type: rounding it by 2^-8
         // of itself at most is what O's own rounding may cost.  l sums it unrounded.
-        const float sc = fabsf(m_run * scale_log2) > kFar ? kFarScale : scale_log2, nm = -m_run * sc;
-        const uint64_t sc2 = f2_pack(sc, sc), nm2 = f2_pack(nm, nm);
+        uint64_t sc2, nm2;
+        P_factors(m_run, scale_log2, sc2, nm2);
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll 1
         for (int half = 0; half * 64 < min(valid, kTile); ++half) {  // P V stops at the last key's 16
@@ -588,7 +563,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
       for (int x = 0; x < 2; ++x) {
         const int tok0 = u.q0 + x * xg.tokens;
         if (tok0 >= u.q1) break;
-        float2 st = make_float2(0.0f, -FLT_MAX);
+        float2 st = make_float2(0.0f, kNoMax);
         if (keys) {
           const uint32_t n = x ? un1++ : un0++;
           if (!wait_for<100>(&stat_full[(n & 1) * 2 + x], (n >> 1) & 1, wu) ||
@@ -607,7 +582,7 @@ cross_fwd_kernel(const __grid_constant__ XMaps m, const CrossArgs a, const XGrid
         if (part_o) {
           if (live) part_lm[((int64_t)u.split * a.H + h) * a.N + tok] = st;
         } else if (a.lse && live) {
-          a.lse[(int64_t)h * a.N + tok] = lse_of(st.x, st.y, DH);
+          a.lse[(int64_t)h * a.N + tok] = lse_of(st.x, st.y, 1.4426950408889634f * rsqrtf((float)DH));
         }
         // l is at least 2^-16, or 0 where every score is -inf: as without keys
         st.x = st.x == 0.0f ? 0.0f : __fdividef(1.0f, st.x);
@@ -707,7 +682,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
   if (!inside) return;
   const int64_t rows = a.N * a.H, at = (int64_t)h * a.N + n;
   const float scale_log2 = 1.4426950408889634f * rsqrtf((float)DH);
-  float m = -FLT_MAX;
+  float m = kNoMax;
   for (int s = lane; s < splits; s += 32) m = fmaxf(m, part_lm[s * rows + at].y);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -717,7 +692,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
     // 32 weights at a time, one a lane; the rows of the shares with keys
     // then come in several at once
     const float2 e = base + lane < splits ? part_lm[(base + lane) * rows + at] : make_float2(0.0f, m);
-    const float f = e.x * moved(e.y, m, scale_log2);
+    const float f = e.x * P_moved(e.y, m, scale_log2);
 #pragma unroll 8
     for (int s = 0; s < min(32, splits - base); ++s) {
       const float g = __shfl_sync(0xffffffffu, f, s);
@@ -730,7 +705,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const CrossArgs a, int 
     }
   }
   store_row<C>(a.out, w * DH, lane, o, l == 0.0f ? 0.0f : 1.0f / l);
-  if (a.lse && lane == 0) a.lse[at] = lse_of(l, m, DH);
+  if (a.lse && lane == 0) a.lse[at] = lse_of(l, m, scale_log2);
 }
 
 

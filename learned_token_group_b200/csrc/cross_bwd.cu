@@ -41,13 +41,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// P = 2^(S scale + neg_lse).  lse is fp32, so P is off by a factor of up to
-// 2^(|lse| 2^-23): a quarter at 2^20, anything from nothing to infinity beyond.
-// Rows past that, and those whose scores are all -inf, take P = 0: they add
-// nothing to any gradient, where they would have added infinities to all.
-constexpr float kMostLse = 1048576.0f;
-__device__ __forceinline__ float neg_lse(float lse) { return fabsf(lse) >= kMostLse ? -INFINITY : -lse * kLog2e; }
-
 struct BMaps {
   CUtensorMap q, dout, out, k, v;
   XView qv, dv, kv, vv;  // out is laid out as dout
@@ -540,7 +533,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
           }
           if (u.split == 0) a.dsum[(int64_t)h * a.N + tok] = D;
         }
-        out[row] = neg_lse(lse);
+        out[row] = neg_lse_log2(lse);
         out[kTile + row] = D;
         mbar_arrive(&vec_full[un & 1]);
         ++un;
@@ -705,7 +698,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
         for (int i = 0; i < 4; ++i) {
           const int r = lane + 32 * i;
           const int64_t at = (int64_t)(head_of(g, loop) + (r & (xg.r - 1))) * a.N + tok + (r >> xg.log2r);
-          lv[i] = r < rows ? neg_lse(a.lse[at]) : -INFINITY;
+          lv[i] = r < rows ? neg_lse_log2(a.lse[at]) : -INFINITY;
           dv[i] = r < rows ? -a.dsum[at] : 0.0f;
         }
       };

@@ -298,6 +298,40 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// ---------------------------------------------------------------- softmax at scores of any size
+// P = 2^(S scale - fl(m scale)) in one fused step, m the running maximum of the
+// scores themselves.  The rounding of m scale is a factor of P that the row sum
+// shares; but it passes 2^128 once m scale is past 2^32, and P would be infinite
+// or 0.  Past kFar two scores that differ do so by |m| 2^-24 at least, 32 in the
+// exponent: the smaller one's weight is nothing in fp32, at half the scale too.
+// There the scale is a power of two, whose products are exact: P = 1 at the
+// maximum.  Only a row's two factors change (subtracting m from every S first
+// cost cross attention 1 to 4 %).  m starts at kNoMax, not at -inf: a tile of
+// scores of -inf then gives P = 0, where -inf - -inf is NaN for all tiles behind.
+constexpr float kFar = 536870912.0f;     // 2^29
+constexpr float kFarScale = 0.125f;      // the power of two below log2(e) / sqrt(64) and log2(e) / sqrt(128)
+constexpr float kNoMax = -3.402823466e38f;
+// 2^((m - to) scale), to >= m: what a sum over P takes as its maximum goes from m
+// to `to`.  Here and in lse_of m scale is rounded as P has it, not fused away.
+__device__ __forceinline__ float P_moved(float m, float to, float scale_log2) {
+  const float ms = __fmul_rn(m, scale_log2);
+  if (fabsf(ms) > kFar) return m == to ? 1.0f : 0.0f;
+  return fast_exp2(ms - __fmul_rn(to, scale_log2));
+}
+// Natural log-sum-exp of the scaled scores from a row's sum and maximum; -inf for a sum of 0.
+__device__ __forceinline__ float lse_of(float l, float m, float scale_log2) {
+  return (__fmul_rn(m, scale_log2) + log2f(l)) * 0.6931471805599453f;
+}
+// -lse log2(e), from which a backward pass forms P = 2^(S scale + it).  lse is
+// fp32, so P is off by a factor of up to 2^(|lse| 2^-23): a quarter at 2^20,
+// anything from nothing to infinity beyond.  Rows past that, and those whose
+// scores are all -inf, take P = 0: they add nothing to any gradient, where they
+// would have added infinities to all.
+constexpr float kMostLse = 1048576.0f;
+__device__ __forceinline__ float neg_lse_log2(float lse) {
+  return fabsf(lse) >= kMostLse ? -__int_as_float(0x7f800000) : -lse * 1.4426950408889634f;
+}
+
 // Packed fp32 pairs (sm_100 f32x2 instructions): one issue slot for two lanes of work.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t r;
@@ -321,6 +355,12 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// Scale and offset of a row's exponents S scale + offset.
+__device__ __forceinline__ void P_factors(float m, float scale_log2, uint64_t& scale2, uint64_t& offset2) {
+  const float sc = fabsf(m * scale_log2) > kFar ? kFarScale : scale_log2, off = -__fmul_rn(m, sc);
+  scale2 = f2_pack(sc, sc);
+  offset2 = f2_pack(off, off);
 }
 // Three-input maximum (sm_100).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

@@ -329,10 +329,10 @@ stga_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
         float mx = m8[0];
 #pragma unroll
         for (int g = 1; g < NSC * 2; ++g) mx = fmaxf(mx, m8[g]);
-        const float m = mx * scale_log2;
+        const float m = fmaxf(mx, kNoMax);
         // P = 2^(S*scale - m) as packed bf16 pairs over S; l = sum of P
-        const uint64_t sc2 = f2_pack(scale_log2, scale_log2);
-        const uint64_t nm2 = f2_pack(-m, -m);
+        uint64_t sc2, nm2;
+        P_factors(m, scale_log2, sc2, nm2);
         uint64_t la = f2_pack(0.f, 0.f), lb = la;
 #pragma unroll
         for (int c = 0; c < NSC; ++c) {
@@ -372,9 +372,9 @@ stga_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUte
             // its row-major index inside the clipped window
             const int start = w.t0 * a.Hg * a.Wg + w.et * (w.h0 * a.Wg + w.eh * w.w0);
             const int pos = start + (rf * w.eh + ri) * w.ew + rj;
-            a.lse[(int64_t)h * a.N + pos] = (m + log2f(l)) * 0.6931471805599453f;
+            a.lse[(int64_t)h * a.N + pos] = lse_of(l, m, scale_log2);
           }
-          const float inv = a.out_scale / l;
+          const float inv = l == 0.0f ? 0.0f : a.out_scale / l;  // 0: every score is -inf
           uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
                                                 (tok * H + h) * (int64_t)DH);
 #pragma unroll
