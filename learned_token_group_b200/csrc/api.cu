@@ -1354,6 +1354,7 @@ moga_status moga_cross_attn_backward(const void* dout, const void* q, int64_t q_
   a.dk = dk;
   a.dv = dv;
   a.fill = fill;
+  a.withhold = g_debug_inject.load(std::memory_order_relaxed) == 1;
   int launches = 0;
   const cudaError_t e = launch_cross_bwd(c, a, (uint8_t*)ws + kHeader, &launches);
   count((uint64_t)launches);

@@ -227,6 +227,7 @@ cross_dq_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid 
         for (int row = u.k0; row < u.k1; row += kTile) {
           const uint32_t s = kt % 3, sv = vt % 2;
           if (!wait_for(&k_empty[s], ((kt / 3) & 1) ^ 1, wc)) { ok = false; break; }
+          if (a.withhold && kt == 0) { ok = false; break; }  // test hook: this tile never comes
           load_tile<DH>(&m.k, m.kv, &k_full[s], smem + P::kK + s * P::T, 1, hk, row, keep);
           ++kt;
           if (!wait_for(&v_empty[sv], ((vt / 2) & 1) ^ 1, wc)) { ok = false; break; }
@@ -631,6 +632,7 @@ cross_dkv_kernel(const __grid_constant__ BMaps m, const CrossArgs a, const XGrid
           for (int tok = u.q0; tok < u.q1; tok += xg.tokens) {
             const uint32_t s1 = t1 % 3, s2 = t2 % 2;
             if (!wait_for(&y1_empty[s1], ((t1 / 3) & 1) ^ 1, wc)) { ok = false; break; }
+            if (a.withhold && t1 == 0) { ok = false; break; }  // test hook: this tile never comes
             load_tile<DH>(&m.q, m.qv, &y1_full[s1], smem + P::kY1 + s1 * P::T, xg.r, h, tok, keep);
             ++t1;
             // A tile comes in when the products of the tile before last are

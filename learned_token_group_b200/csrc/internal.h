@@ -196,7 +196,7 @@ struct CrossArgs {
   void* dv;
   float* dsum;            // [H, N]
   int fill;               // rows of no segment: out (dq) = 0 and lse = -inf; otherwise left as they were
-  int withhold;           // test hook: the forward's first K tile never comes
+  int withhold;           // test hook: a CTA's first K (dK, dV: Q) tile never comes
 };
 size_t cross_fwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);
 size_t cross_bwd_ws_bytes(int64_t N, int64_t L, int H, int H_kv, int d_h, int S);

@@ -778,3 +778,28 @@ def test_a_unit_longer_than_the_wait_limit():
     finally:
         lib.moga_set_wait_limit_ns(old)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("N,L,H,Hk", [(500, 300, 2, 2), (5, 3000, 2, 2), (200, 38400, 2, 1)])
+def test_a_wait_that_runs_out_in_the_backward_is_reported_and_the_next_call_is_right(N, L, H, Hk):
+    """The test hook withholds each CTA's first K tile (dQ) or Q tile (dK, dV): the bounded waits run out, nothing hangs."""
+    lib = moga.get_lib()
+    c = Case([N], [L], H, Hk, 64)
+    seg = dict(q_offsets=ints([0, N]))                # dk and dv then start as zeros
+    out, lse = moga.cross_attn(*c.in_place, return_lse=True)
+    ws = moga.workspace(moga.cross_attn_workspace_size(c.q, c.k, backward=True), "cuda")
+    old = lib.moga_set_wait_limit_ns(50_000_000)
+    try:
+        assert lib.moga_debug_inject(1) == 0
+        g = moga.cross_attn_backward(c.dout, *c.in_place, out, lse, **seg, ws=ws)
+        with pytest.raises(moga.MogaError) as e:
+            moga.sync_status(ws)
+        assert e.value.status == TIMEOUT
+        if L > 38000:                                 # one share of the queries: nothing adds up what was not written
+            assert (g["dk"] == 0).all() and (g["dv"] == 0).all()
+    finally:
+        lib.moga_debug_inject(0)
+        lib.moga_set_wait_limit_ns(old)
+    moga.sync_status(ws)
+    check_backward(c, out, lse, ws=ws)
+    moga.sync_status(ws)
