@@ -887,8 +887,9 @@ class CrossAttnFunction(torch.autograd.Function):
     def forward(ctx, q, k, v, q_offsets=None, kv_offsets=None, kv_lens=None, ws=None):
         q, k, v = (_readable(t, head_major=True) for t in (q, k, v))
         if ws is not None:
-            S = max([1] + [t.numel() - 1 for t in (q_offsets, kv_offsets) if t is not None])
-            _enough(ws, cross_attn_workspace_size(q, k, S, backward=True))
+            _, sizes, _ = _cross_setup(q, k, v, q_offsets, kv_offsets, kv_lens)
+            _enough(ws, max(get_lib().moga_cross_attn_workspace_size(*sizes),
+                            get_lib().moga_cross_attn_backward_workspace_size(*sizes)))
         out, lse = cross_attn(q, k, v, q_offsets, kv_offsets, kv_lens, return_lse=True, ws=ws)
         ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets, kv_lens)
         ctx.ws = ws

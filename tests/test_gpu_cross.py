@@ -803,3 +803,14 @@ def test_a_wait_that_runs_out_in_the_backward_is_reported_and_the_next_call_is_r
     moga.sync_status(ws)
     check_backward(c, out, lse, ws=ws)
     moga.sync_status(ws)
+
+
+def test_autograd_with_a_workspace_refuses_as_the_call_does():
+    q, k = (torch.zeros(n, 2, 64, dtype=torch.bfloat16, device="cuda") for n in (10, 8))
+    ws = moga.workspace(1 << 20, "cuda")
+    for bad in ((q[0], k, k), (q, k[0], k), (q, k[:, :0], k[:, :0]), (q, k, k, ints([0]), ints([0]))):
+        args = list(bad) + [None] * (6 - len(bad))
+        with pytest.raises((ValueError, moga.MogaError)):
+            moga.CrossAttnFunction.apply(*args)
+        with pytest.raises((ValueError, moga.MogaError)):
+            moga.CrossAttnFunction.apply(*args, ws)
