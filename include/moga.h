@@ -387,7 +387,9 @@ moga_status moga_layer_ex(const void* x, const void* W_r, const float* b_r, moga
  *      axes is HOST int[3].
  * Out: q_out, k_out bf16 [N, H, d_h], dense.  A bf16, dense input may be its
  *      own output; any other overlap is not allowed.
- * The sums and the rotation are fp32; an output is rounded once.
+ * The sums and the rotation are fp32; an output is rounded once.  A row with a
+ * channel past 2^60, whose sum of squares fp32 does not hold, gives 0; so small
+ * a one (2^-60) is 0 to fp32 too, which matters with eps = 0 alone.
  * Limits: d_h 64 or 128, H up to 65536, eps >= 0 and finite.
  * Workspace: moga_qk_norm_rope_workspace_size() bytes, needed with pos only
  * (ws may be NULL otherwise). */

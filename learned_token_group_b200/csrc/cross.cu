@@ -30,11 +30,14 @@
 //           memory per warp to 128-byte row pieces.  Prompts are short: with 512
 //           keys a unit has four steps, and an epilogue inside the softmax warps
 //           would take as long as two of them.
-// Measured at 187,200 x 512 keys, 12 heads of 128 channels: 0.57 ms, 1.03
-// PFLOP/s (0.62 of the measured cuBLAS burst; 0.66 ms in a long run under the
-// power cap); x 128 keys: 0.24 ms, 4.8 TB/s.  Bound by the issue of products
-// (about 100 cycles an instruction against 64 of math) with long prompts, by
-// HBM and the epilogue with short ones.
+// Measured at 187,200 x 512 keys, 12 heads of 128 channels: 0.55 to 0.57 ms,
+// 1.05 PFLOP/s (0.63 of the measured cuBLAS burst; 0.67 ms in a long run under
+// the power cap); of 64 channels 0.46 to 0.48 ms; x 128 keys of 128: 0.24 to
+// 0.25 ms, 4.7 TB/s, near HBM's rate.  With long prompts no unit is full: a step
+// of two query tiles and 128 keys takes 3,990 cycles, of which the products are
+// 51 % (29 % at 64 channels) and the exponentials 52 % (57 %), instructions issue
+// in 43 %, and 7 % of instruction fetches miss.  Softmax and products take turns
+// more than they overlap; which wait makes up the rest is not measured.
 // With few units the key range is split over CTAs, which write O / l and (l, m)
 // in fp32, and cross_join_kernel joins them.
 // How P keeps clear of infinities at scores of any size: P_factors in ptx.cuh.

@@ -18,9 +18,11 @@
 // needs none.  A warp's item is one token and up to kRows rows per lane group
 // of its query heads or of its key heads, all loaded before the first is
 // used; the cosines and sines are read once for those rows.  Measured at
-// 187,200 tokens of 24 heads, 128 channels, bf16 with rotation: forward 383 to 399 us
-// (5.8 to 6.0 TB/s, 0.88 to 0.92 of the measured copy rate), gradients 608 to
-// 633 us (5.5 to 5.7 TB/s).
+// 187,200 tokens of 24 heads, 128 channels, bf16 with rotation: forward 383 to 416 us
+// (5.5 to 6.0 TB/s, 0.84 to 0.92 of the measured copy rate), gradients 608 to
+// 633 us (5.5 to 5.7 TB/s); fp32 at 62,400 tokens: 204 and 313 us (5.6 and 6.1
+// TB/s).  The register limits (64 forward, 128 gradients) cost the bf16 instances
+// 4 to 16 bytes of spills a thread.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
