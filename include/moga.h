@@ -388,8 +388,9 @@ moga_status moga_layer_ex(const void* x, const void* W_r, const float* b_r, moga
  * Out: q_out, k_out bf16 [N, H, d_h], dense.  A bf16, dense input may be its
  *      own output; any other overlap is not allowed.
  * The sums and the rotation are fp32; an output is rounded once.  A row with a
- * channel past 2^60, whose sum of squares fp32 does not hold, gives 0; so small
- * a one (2^-60) is 0 to fp32 too, which matters with eps = 0 alone.
+ * sum of squares past fp32's largest number (a channel past 2^60 at the
+ * earliest) gives 0 and gradients of 0; with eps = 0 one whose squares are all
+ * below fp32's normal numbers (channels below 2^-63) has no length to divide by.
  * Limits: d_h 64 or 128, H up to 65536, eps >= 0 and finite.
  * Workspace: moga_qk_norm_rope_workspace_size() bytes, needed with pos only
  * (ws may be NULL otherwise). */

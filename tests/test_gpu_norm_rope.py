@@ -453,3 +453,19 @@ def test_autograd_takes_gradients_that_start_anywhere(first):
     got = torch.autograd.grad(moga.QkNormRopeFunction.apply(*args), [a["q"], a["k"]], [dq, dk])
     want = torch.autograd.grad(moga.QkNormRopeFunction.apply(*args), [a["q"], a["k"]], [dq.clone(), dk.clone()])
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_too_large_for_their_sum_give_zero(dtype):
+    """A sum of squares past fp32's range: 1 / sqrt(inf) = 0.  The other rows are as ever."""
+    a, ang = make(20, 2, 2, 64, dtype, "dense", "grid")
+    a["q"][7, 1] *= 1e25
+    out = moga.qk_norm_rope(**a)
+    dy = [torch.ones(t.shape, dtype=torch.bfloat16, device="cuda") for t in out]
+    g = moga.qk_norm_rope_backward(*dy, **a)
+    assert (out[0][7, 1] == 0).all() and (g["dq"][7, 1] == 0).all() and torch.isfinite(g["dw_q"]).all()
+    a["q"][7, 1] = 1
+    near(out[1], *around.norm_rope(a["k"], a["w_k"], EPS, ang, False), FWD, HALF[torch.bfloat16])
+    want, size = around.norm_rope(a["q"], a["w_q"], EPS, ang, False)
+    keep = [n for n in range(20) if n != 7]
+    near(out[0][keep], want[keep], size[keep], FWD, HALF[torch.bfloat16])
